@@ -1,5 +1,5 @@
 """Python binding of libmoe_b200 (one MoE expert layer with groupwise-affine
-4-bit weights on B200).
+4-bit weights on B200, and the token mixers beside it).
 
 Argument marshalling only: every step of the layer runs in the CUDA library.
 The functions carry the C ABI's names (``include/moe_b200.h``); tensors are
@@ -45,8 +45,15 @@ EXPORTED = (
     "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_permute", "moe_expert_ffn",
     "moe_expert_ffn_path", "moe_combine", "moe_get_device_error", "moe_status_string", "moe_launch_count",
     "moe_permute_static", "moe_decode_layer", "moe_wait_selftest", "moe_gather_rows", "gdn_scan",
-    "moe_router_logits",
+    "moe_router_logits", "attn_qkv_prepare", "attn_kv_read", "attn_prefill", "attn_decode_workspace_size",
+    "attn_decode",
 )
+
+ATTN_CACHE_BF16 = 0
+ATTN_CACHE_E4M3 = 1
+
+ATTN_ROPE_HALF = 0
+ATTN_ROPE_PAIRS = 1
 
 MOE_STATIC_MAX_TOKENS = 16384
 
@@ -60,8 +67,19 @@ def config(hidden=2048, inter=512, num_experts=256, top_k=8, group_size=64, has_
     return moe_config_t(hidden, inter, num_experts, top_k, group_size, has_shared)
 
 
+class attn_config_t(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("cache_type", ctypes.c_int32)]
+
+
+def attn_config(q_heads=16, kv_heads=2, head_dim=128, page_size=64, cache_type=ATTN_CACHE_BF16) -> attn_config_t:
+    return attn_config_t(q_heads, kv_heads, head_dim, page_size, cache_type)
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 _CFG = ctypes.POINTER(moe_config_t)
 
 _lib.moe_workspace_size.restype = ctypes.c_size_t
@@ -83,6 +101,18 @@ _lib.moe_combine.restype = _I32
 _lib.moe_combine.argtypes = [_CFG, _I32, _I32, _P, _P, _P, _P, _P, _P]
 _lib.gdn_scan.restype = _I32
 _lib.gdn_scan.argtypes = [_I32] * 6 + [_P] * 5 + [ctypes.c_float, _P, _P, _P, _P]
+_ACFG = ctypes.POINTER(attn_config_t)
+_lib.attn_qkv_prepare.restype = _I32
+_lib.attn_qkv_prepare.argtypes = [_ACFG, _I32, _P, _I64, _P, _P, _F32, _P, _I32, _I32, _F32, _P, _P, _I32] + [_P] * 8
+_lib.attn_kv_read.restype = _I32
+_lib.attn_kv_read.argtypes = [_ACFG, _I32, _I32, _P, _I64, _P, _I32] + [_P] * 8
+_lib.attn_prefill.restype = _I32
+_lib.attn_prefill.argtypes = [_ACFG, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _F32, _I32] + [_P] * 4
+_lib.attn_decode_workspace_size.restype = ctypes.c_size_t
+_lib.attn_decode_workspace_size.argtypes = [_ACFG, _I32, _I32, _I32]
+_lib.attn_decode.restype = _I32
+_lib.attn_decode.argtypes = [_ACFG, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _F32, _P, _P, _P,
+                             ctypes.c_size_t, _P, _P]
 _lib.moe_gather_rows.restype = _I32
 _lib.moe_gather_rows.argtypes = [_CFG, _I32, _P, _P, _P, _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]
 _lib.moe_get_device_error.restype = _I32
@@ -211,6 +241,82 @@ def gdn_scan(B, T, Hk, Hv, dk, dv, q, k, v, g, beta, scale, state_in, state_out,
     return _check(st, "gdn_scan", raise_on_error)
 
 
+def _dptr(t, name: str, dtypes: tuple, rows: bool = False) -> int | None:
+    """_ptr of a tensor on the GPU, of one of these types and contiguous (rows:
+    contiguous within its first dimension's rows)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("%s is on %s, not on a GPU" % (name, t.device))
+    if str(t.dtype)[6:] not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(dtypes), t.dtype))
+    if not t.is_contiguous() and not (rows and t.numel() and t[0].is_contiguous()):
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+_BF16 = ("bfloat16",)
+_FP32 = ("float32",)
+_INT32 = ("int32",)
+_CACHE = {ATTN_CACHE_BF16: ("bfloat16",), ATTN_CACHE_E4M3: ("float8_e4m3fn", "uint8")}
+
+
+def _cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale) -> tuple:
+    kind = _CACHE.get(cfg.cache_type, ())
+    return (_dptr(k_cache, "k_cache", kind), _dptr(v_cache, "v_cache", kind), _dptr(k_scale, "k_scale", _FP32),
+            _dptr(v_scale, "v_scale", _FP32))
+
+
+def attn_qkv_prepare(cfg, T, qkv, qkv_stride, q_weight, k_weight, eps, inv_freq, rot_dim, rope_layout, rope_scale,
+                     positions, slots, num_pages, k_cache, v_cache, k_scale, v_scale, q_out, k_out, err=None,
+                     stream=None, raise_on_error=True) -> int:
+    """Norm of queries and keys, rotation of their positions, cache write (include/attn_b200.h)."""
+    st = _lib.attn_qkv_prepare(ctypes.byref(cfg), T, _dptr(qkv, "qkv", _BF16, True), qkv_stride,
+                               _dptr(q_weight, "q_weight", _BF16), _dptr(k_weight, "k_weight", _BF16), eps,
+                               _dptr(inv_freq, "inv_freq", _FP32), rot_dim, rope_layout, rope_scale,
+                               _dptr(positions, "positions", _INT32), _dptr(slots, "slots", _INT32), num_pages,
+                               *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), _dptr(q_out, "q_out", _BF16),
+                               _dptr(k_out, "k_out", _BF16), _dptr(err, "err", _INT32), _stream(stream))
+    return _check(st, "attn_qkv_prepare", raise_on_error)
+
+
+def attn_kv_read(cfg, B, total, page_table, page_table_stride, cu_lens, num_pages, k_cache, v_cache, k_scale, v_scale,
+                 k_out, v_out, err=None, stream=None, raise_on_error=True) -> int:
+    """The cache's rows of each sequence, packed, in bf16 (include/attn_b200.h)."""
+    st = _lib.attn_kv_read(ctypes.byref(cfg), B, total, _dptr(page_table, "page_table", _INT32, True),
+                           page_table_stride, _dptr(cu_lens, "cu_lens", _INT32), num_pages,
+                           *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), _dptr(k_out, "k_out", _BF16),
+                           _dptr(v_out, "v_out", _BF16), _dptr(err, "err", _INT32), _stream(stream))
+    return _check(st, "attn_kv_read", raise_on_error)
+
+
+def attn_prefill(cfg, B, total_q, total_k, cu_q, cu_k, q, q_stride, k, k_stride, v, v_stride, scale, causal, out,
+                 lse=None, err=None, stream=None, raise_on_error=True) -> int:
+    """Attention over packed prompts (include/attn_b200.h)."""
+    st = _lib.attn_prefill(ctypes.byref(cfg), B, total_q, total_k, _dptr(cu_q, "cu_q", _INT32),
+                           _dptr(cu_k, "cu_k", _INT32), _dptr(q, "q", _BF16, True), q_stride, _dptr(k, "k", _BF16, True),
+                           k_stride, _dptr(v, "v", _BF16, True), v_stride, scale, int(causal), _dptr(out, "out", _BF16),
+                           _dptr(lse, "lse", _FP32), _dptr(err, "err", _INT32), _stream(stream))
+    return _check(st, "attn_prefill", raise_on_error)
+
+
+def attn_decode_workspace_size(cfg, B: int, nq: int, max_len: int) -> int:
+    return int(_lib.attn_decode_workspace_size(ctypes.byref(cfg), B, nq, max_len))
+
+
+def attn_decode(cfg, B, nq, max_len, q, q_stride, page_table, page_table_stride, seq_lens, num_pages, k_cache, v_cache,
+                k_scale, v_scale, scale, out, lse, ws, ws_bytes=None, err=None, stream=None,
+                raise_on_error=True) -> int:
+    """Attention of a few new tokens per sequence over the cache (include/attn_b200.h)."""
+    n = _nbytes(ws) if ws_bytes is None else ws_bytes
+    st = _lib.attn_decode(ctypes.byref(cfg), B, nq, max_len, _dptr(q, "q", _BF16, True), q_stride,
+                          _dptr(page_table, "page_table", _INT32, True), page_table_stride,
+                          _dptr(seq_lens, "seq_lens", _INT32), num_pages,
+                          *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), scale, _dptr(out, "out", _BF16),
+                          _dptr(lse, "lse", _FP32), _ptr(ws), n, _dptr(err, "err", _INT32), _stream(stream))
+    return _check(st, "attn_decode", raise_on_error)
+
+
 def moe_decode_layer(cfg, T, x, w_router, logit_bias, logit_bias_row_stride, gu_codes, gu_sb, d_codes, d_sb,
                      topk_idx, topk_w, counts, offsets, row_to_pair, pair_to_row, y_acc, y, ws, ws_bytes=None,
                      stream=None, raise_on_error=True) -> int:
@@ -250,4 +356,5 @@ def moe_wait_selftest(kind: int, ctas: int, skip_cta: int, limit_ns: int, ws, st
     return _check(st, "moe_wait_selftest", raise_on_error)
 
 
+from .attention import AttentionLayer  # noqa: E402  (torch-level wrapper of the attention operators)
 from .layer import MoELayer  # noqa: E402  (torch-level convenience wrapper)

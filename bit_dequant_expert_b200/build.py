@@ -41,7 +41,7 @@ def nvcc() -> str:
 
 def _deps() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) +
-                  [os.path.join(INCLUDE, "moe_b200.h")])
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def sources() -> list[str]:

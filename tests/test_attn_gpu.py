@@ -1,0 +1,576 @@
+"""The attention operators against their plain 64-bit forms (tests/attn_ref.py
+derives the attention tolerances)."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as R
+import bit_dequant_expert_b200 as m
+
+pytestmark = pytest.mark.gpu
+
+
+def rng(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def err_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ prepare
+
+
+def prepare_case(T, hq, hkv, dim, rot, layout, e4m3, page, seed, scale=1.0, norm=True, first=0, extra=0, skip=False):
+    g = rng(seed)
+    qkv = (torch.randn(T, (hq + 2 * hkv) * dim + extra, generator=g) * 3).bfloat16()
+    qw, kw = ((1 + 0.2 * torch.randn(dim, generator=g)).bfloat16() for _ in range(2))
+    if not norm:
+        qw = kw = None
+    inv = torch.pow(10000.0, -torch.arange(0, rot, 2).double() / max(rot, 1)).float() if rot else None
+    pos = (torch.arange(T) * 3 + first).int()
+    pages = (T + page - 1) // page + 1
+    slots = torch.randperm(pages * page, generator=g)[:T].int()
+    if skip:
+        slots[::3] = -1
+    return dict(qkv=qkv, qw=qw, kw=kw, inv=inv, pos=pos, slots=slots, pages=pages, rs=scale)
+
+
+def run_prepare(c, d, T, rot, layout, k_out=True, slots=True, err=None, stride=None):
+    hq, hkv, dim, page = c.q_heads, c.kv_heads, c.head_dim, c.page_size
+    e4m3 = c.cache_type == m.ATTN_CACHE_E4M3
+    shape = (d["pages"], hkv, page, dim)
+    fill = 7.0   # what is not written stays
+    kc, vc = (torch.full(shape, fill, device="cuda").to(torch.float8_e4m3fn if e4m3 else torch.bfloat16) for _ in "kv")
+    ks, vs = (torch.full(shape[:3], fill, device="cuda") if e4m3 else None for _ in "kv")
+    q = torch.full((T, hq, dim), math.nan, dtype=torch.bfloat16, device="cuda")
+    k = torch.full((T, hkv, dim), math.nan, dtype=torch.bfloat16, device="cuda") if k_out else None
+    qkv, qw, kw, inv, pos, sl = R.cuda(d["qkv"], d["qw"], d["kw"], d["inv"], d["pos"], d["slots"])
+    m.attn_qkv_prepare(c, T, qkv, qkv.stride(0), qw, kw, 1e-6, inv, rot, layout, d["rs"], pos, sl if slots else None,
+                       d["pages"], kc, vc, ks, vs, q, k, err=err)
+    torch.cuda.synchronize()
+    return q, k, kc, vc, ks, vs
+
+
+def check_prepared(c, d, T, rot, layout, got):
+    hq, hkv, dim, page = c.q_heads, c.kv_heads, c.head_dim, c.page_size
+    (q, qs), (k, ksz), v = R.prepared(d["qkv"][:, :(hq + 2 * hkv) * dim], hq, hkv, dim, d["qw"], d["kw"], 1e-6,
+                                      d["inv"], rot, layout, d["rs"], d["pos"])
+    gq, gk, kc, vc, ks, vs = [None if t is None else t.cpu() for t in got]
+    # fp32 arithmetic: the sum of squares of up to 256 terms, the root and its product, the angle and two products:
+    # under 2^-18 of the sizes; then one rounding, half a step
+    def close(x, ref, size):
+        off = (x.double() - ref).abs() - (2.0 ** -8 * ref.abs() + 2.0 ** -18 * size)
+        assert off.max() <= 0, "off by %.3e more than allowed" % off.max()
+
+    close(gq, q, qs)
+    if gk is not None:
+        close(gk, k, ksz)
+    slots = d["slots"].long()
+    live = slots >= 0
+    p, o = slots[live] // page, slots[live] % page
+    touched = torch.zeros(d["pages"], page, dtype=torch.bool)
+    touched[p, o] = True
+    for cache, scale, ref, size in ((kc, ks, k, ksz), (vc, vs, v, v.abs())):
+        rows = cache.float()[p, :, o].double()
+        ref, size = ref[live], size[live]
+        if scale is None:
+            off = (rows - ref).abs() - (2.0 ** -8 * ref.abs() + 2.0 ** -18 * size)
+        else:
+            s = scale[p, :, o].double()
+            want = ref.abs().amax(-1) / 448
+            want = torch.where(want > 0, want, torch.ones_like(want))
+            assert ((s - want).abs() <= 2.0 ** -18 * want + 2.0 ** -18 * size.amax(-1) / 448).all()
+            # half a step of e4m3: 2^-4 of the value, or 2^-10 of the scale among the subnormals
+            half = torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * s[..., None])
+            off = (rows * s[..., None] - ref).abs() - half * (1 + 2.0 ** -16) - 2.0 ** -17 * size
+        assert off.numel() == 0 or off.max() <= 0, "cache off by %.3e more than allowed" % off.max()
+        assert (cache.float().transpose(1, 2)[~touched] == 7.0).all(), "rows outside the slots changed"
+
+
+@pytest.mark.parametrize("T,hq,hkv,dim,rot,layout,e4m3,page,kw", [
+    (1, 16, 2, 128, 128, 0, True, 64, {}),
+    (1, 16, 2, 256, 64, 0, False, 16, dict(first=1_000_003)),
+    (7, 5, 1, 64, 64, 1, True, 16, dict(norm=False)),
+    (33, 12, 4, 128, 48, 1, False, 128, dict(scale=1.2, extra=24)),
+    (300, 8, 8, 64, 16, 0, True, 32, dict(skip=True)),
+    (65, 16, 2, 256, 256, 0, True, 16, dict(first=2_000_000_000, scale=0.7)),
+    (50, 3, 3, 128, 0, 0, True, 64, {}),
+    (2500, 16, 2, 128, 128, 1, True, 64, dict(first=65536)),
+    (1300, 32, 8, 64, 32, 0, False, 32, dict(skip=True)),
+])
+def test_prepare(T, hq, hkv, dim, rot, layout, e4m3, page, kw):
+    c = m.attn_config(hq, hkv, dim, page, int(e4m3))
+    d = prepare_case(T, hq, hkv, dim, rot, layout, e4m3, page, T + dim, **kw)
+    got = run_prepare(c, d, T, rot, layout)
+    check_prepared(c, d, T, rot, layout, got)
+    # without the keys' copy, and without a cache: the same outputs
+    q, k, *_ = run_prepare(c, d, T, rot, layout, k_out=False)
+    assert k is None and torch.equal(q, got[0])
+    q, k, kc, *_ = run_prepare(c, d, T, rot, layout, slots=False)
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1]) and (kc.float() == 7.0).all()
+
+
+def test_prepare_edge_rows_and_bad_slots():
+    """A row of zeros (scale 1, codes 0), rows with an infinity or NaN (scale
+    NaN), tiny and huge rows, and slots past the cache (reported, skipped)."""
+    c = m.attn_config(4, 2, 128, 16, m.ATTN_CACHE_E4M3)
+    d = prepare_case(8, 4, 2, 128, 0, 0, True, 16, 3, norm=False)
+    rows = d["qkv"].view(8, 8, 128)
+    rows[0, 4:] = 0
+    rows[1, 4:, 5] = math.inf
+    rows[2, 6:, 7] = math.nan
+    rows[3, 4:] *= 1e-38
+    rows[4, 4:] *= 1e37
+    d["slots"] = torch.tensor([0, 1, 2, 3, 4, 5, d["pages"] * 16, 2 ** 31 - 1], dtype=torch.int32)
+    err = err_word()
+    q, k, kc, vc, ks, vs = run_prepare(c, d, 8, 0, 0, err=err)
+    assert err.item() == m.MOE_ERR_BOUNDS
+    assert torch.equal(q.cpu(), rows[:, :4])
+    assert (ks[0, :, 0] == 1).all() and (vs[0, :, 0] == 1).all() and (kc.float()[0, :, 0] == 0).all()
+    assert ks[0, :, 1].isnan().all() and vs[0, :, 1].isnan().all()
+    assert vs[0, :, 2].isnan().all() and not ks[0, :, 2].isnan().any()
+    for t in (3, 4, 5):
+        ref = rows[t, 4:6].double()
+        got = (kc.float()[0, :, t].double() * ks[0, :, t, None].double()).cpu()
+        assert ((got - ref).abs() <= 2.0 ** -4 * ref.abs() * 1.0001 + ks[0, :, t, None].cpu().double() * 2.0 ** -10 + 1.5e-45 * 448).all()
+    assert (kc.float()[0, :, 6:] == 7.0).all()
+
+
+# ------------------------------------------------------------------ read
+
+
+@pytest.mark.parametrize("lens,hkv,dim,e4m3,page", [
+    ([1], 2, 128, True, 64), ([0, 33, 0, 1, 128, 0], 1, 64, True, 16), ([257, 64, 63], 8, 256, False, 32),
+    ([777], 2, 256, True, 128), ([5, 700, 31, 1], 3, 128, False, 64), (list(range(0, 40)), 2, 64, False, 16)])
+def test_read(lens, hkv, dim, e4m3, page):
+    g = rng(sum(lens))
+    table, pages = R.make_table(g, lens, page)
+    kc, vc, ks, vs = R.make_cache(g, pages, hkv, page, dim, e4m3)
+    total = sum(lens)
+    cu = R.starts(lens) + 2      # two rows before the first sequence and three after the last stay
+    c = m.attn_config(hkv, hkv, dim, page, int(e4m3))
+    k = torch.full((total + 5, hkv, dim), 9.0, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    tb, cu_d, kd, vd, ksd, vsd = R.cuda(table, cu, kc, vc, ks, vs)
+    err = err_word()
+    m.attn_kv_read(c, len(lens), total + 5, tb, tb.stride(0), cu_d, pages, kd, vd, ksd, vsd, k, v, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    for got, cache, scale in ((k, kc, ks), (v, vc, vs)):
+        ref = torch.cat([R.rows_of(cache, scale, table[b], n) for b, n in enumerate(lens)])
+        got = got.cpu()
+        assert (got[:2] == 9.0).all() and (got[total + 2:] == 9.0).all()
+        # the product code * scale has one fp32 rounding (2^-24) before the one to bf16
+        assert ((got[2:total + 2].double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -23) * ref.abs()).all()
+
+
+def test_read_reports_bad_pages_and_lengths():
+    g = rng(1)
+    table, pages = R.make_table(g, [40, 40], 16)
+    kc, vc, _, _ = R.make_cache(g, pages, 2, 16, 64, False)
+    c = m.attn_config(2, 2, 64, 16, 0)
+    table[0, 1], table[1, 0] = pages, -1
+    tb, kd, vd = R.cuda(table, kc, vc)
+
+    def call(cu, total):
+        err = err_word()
+        k = torch.full((total, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+        v = k.clone()
+        m.attn_kv_read(c, 2, total, tb, 3, torch.tensor(cu, dtype=torch.int32).cuda(), pages, kd, vd, None, None, k, v,
+                       err=err)
+        torch.cuda.synchronize()
+        return err.item(), k.cpu()
+
+    status, k = call([0, 40, 80], 80)
+    assert status == m.MOE_ERR_BOUNDS and (k[16:32] == 0).all() and (k[40:56] == 0).all()
+    assert torch.equal(k[:16], kc[table[0, 0].long()].transpose(0, 1))
+    table[0, 1], table[1, 0] = 0, 1
+    tb.copy_(table)
+    assert call([0, 40, 80], 80)[0] == 0
+    assert call([0, 40, 80], 70)[0] == m.MOE_ERR_BOUNDS       # more rows than the outputs hold
+    status, k = call([0, 49, 80], 80)                         # longer than its row of pages
+    assert status == m.MOE_ERR_BOUNDS and (k[48] == 0).all()
+
+
+# ------------------------------------------------------------------ prefill
+
+
+def prefill_limit(nq, nk, causal):
+    return [max(0, min(nk, nk - nq + i + 1)) if causal else nk for i in range(nq)]
+
+
+def run_prefill(lens_q, lens_k, hq, hkv, dim, causal, seed, gain=1.5, pad=0, scale=None, data=None):
+    g = rng(seed)
+    tq, tk = sum(lens_q), sum(lens_k)
+    q = (torch.randn(tq + 3, hq, dim, generator=g) * gain).bfloat16()
+    k = (torch.randn(tk + 2, hkv, dim, generator=g) * gain).bfloat16()
+    v = torch.randn(tk + 2, hkv, dim, generator=g).bfloat16()
+    if data:
+        data(q, k, v)
+    scale = dim ** -0.5 if scale is None else scale
+    cu_q, cu_k = R.starts(lens_q) + 1, R.starts(lens_k) + 2   # rows before and behind belong to nobody
+    c = m.attn_config(hq, hkv, dim)
+    wide = lambda t, w: torch.cat([t.flatten(1), torch.full((t.shape[0], w), math.nan).bfloat16()], 1).cuda()  # noqa: E731
+    qd, kd, vd = wide(q, pad), wide(k, 2 * pad), wide(v, pad)
+    out = torch.full((tq + 3, hq, dim), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((tq + 3, hq), 5.0, device="cuda")
+    err = err_word()
+    m.attn_prefill(c, len(lens_q), tq + 3, tk + 2, cu_q.cuda(), cu_k.cuda(), qd, qd.stride(0), kd, kd.stride(0), vd,
+                   vd.stride(0), scale, causal, out, lse, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    for t in (out, lse):
+        assert (t[:1] == 5.0).all() and (t[tq + 1:] == 5.0).all(), "rows of no sequence changed"
+    for b in range(len(lens_q)):
+        r, s = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        if lens_q[b]:
+            ref = R.attend(q[r], k[s], v[s], scale, prefill_limit(lens_q[b], lens_k[b], causal))
+            R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+    return out, lse
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens_q,lens_k,hq,hkv", [
+    ([1], [1], 2, 1),
+    ([127], [127], 2, 2),
+    ([128], [128], 4, 1),
+    ([129], [129], 1, 1),
+    ([300], [300], 16, 2),
+    ([1, 64, 0, 200, 3], [1, 64, 0, 200, 3], 4, 2),
+    ([5, 130, 17], [400, 131, 257], 3, 1),            # chunks after a prefix; three heads of one key head
+    ([200, 40, 7], [60, 0, 3], 2, 1),                 # fewer keys than queries, and none at all
+    ([513], [1030], 5, 1),
+    ([255, 256, 257], [255, 256, 257], 6, 2),
+])
+def test_prefill(lens_q, lens_k, hq, hkv, dim, causal):
+    run_prefill(lens_q, lens_k, hq, hkv, dim, causal, seed=sum(lens_q) + dim)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_strides_and_scales(dim):
+    run_prefill([70, 130], [70, 200], 4, 2, dim, True, 5, pad=40)
+    run_prefill([70, 130], [70, 200], 4, 2, dim, True, 6, gain=6.0)              # one key takes nearly all
+    run_prefill([150], [300], 2, 2, dim, False, 7, scale=-0.1)
+    run_prefill([150], [300], 2, 2, dim, False, 7, scale=0.0)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_rising_scores(dim):
+    """Scores that grow along the keys by hundreds, so that the running maximum
+    moves in every tile; and keys far below the rest."""
+    def rising(q, k, v):
+        q[:] = 0
+        q[..., 0] = 8
+        k[..., 0] = torch.arange(k.shape[0])[:, None] * 0.5
+
+    run_prefill([200], [600], 2, 1, dim, False, 8, scale=0.25, data=rising)
+    run_prefill([600], [600], 2, 1, dim, True, 9, scale=0.25, data=rising)
+    run_prefill([600], [600], 2, 1, dim, True, 10, scale=-0.25, data=rising)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_neighbours_do_not_leak(dim):
+    """Rows of no sequence and of other sequences that hold NaN and infinities
+    change nothing."""
+    lens = [100, 60, 200]
+
+    def poison(q, k, v):
+        for t in (k, v):
+            t[0], t[1] = math.nan, math.inf
+            t[102:162] = math.nan          # the middle sequence's rows
+            t[362:] = math.nan             # behind the last sequence
+
+    g = rng(11)
+    q = torch.randn(363, 4, dim, generator=g).bfloat16()
+    k, v = (torch.randn(365, 2, dim, generator=g).bfloat16() for _ in "kv")
+    clean = [t.clone() for t in (k, v)]
+    poison(q, k, v)
+    c = m.attn_config(4, 2, dim)
+    cu_q, cu_k = (R.starts(lens) + 1).cuda(), (R.starts(lens) + 2).cuda()
+    outs = []
+    for kk, vv in (clean, (k, v)):
+        qd, kd, vd = R.cuda(q, kk, vv)
+        out = torch.zeros(363, 4, dim, dtype=torch.bfloat16, device="cuda")
+        m.attn_prefill(c, 3, 363, 365, cu_q, cu_k, qd, 4 * dim, kd, 2 * dim, vd, 2 * dim, 0.1, True, out)
+        torch.cuda.synchronize()
+        outs.append(out.cpu())
+    assert torch.equal(outs[0][:101], outs[1][:101]) and torch.equal(outs[0][161:], outs[1][161:])
+    assert outs[1][101:161].isnan().all()
+
+
+def test_prefill_reports_bad_boundaries():
+    c = m.attn_config(2, 1, 64)
+    q, k = torch.ones(20, 2, 64, device="cuda").bfloat16(), torch.ones(20, 1, 64, device="cuda").bfloat16()
+    for cu_q, cu_k in (([0, 10, 20], [0, 10, 21]), ([0, 10, 20], [0, 10, 5]), ([0, 10, 21], [0, 10, 20]),
+                       ([0, 10, 20], [-1, 0, 20]), ([-5, 10, 20], [0, 10, 20]), ([0, 10, 4], [0, 10, 20])):
+        out = torch.full((20, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        err = err_word()
+        m.attn_prefill(c, 2, 20, 20, *(torch.tensor(t, dtype=torch.int32).cuda() for t in (cu_q, cu_k)), q, 128, k, 64,
+                       k, 64, 0.1, False, out, err=err)
+        torch.cuda.synchronize()
+        assert err.item() == m.MOE_ERR_BOUNDS
+        bad_first = cu_q[0] < 0 or cu_k[0] < 0
+        assert (out[:10] == (5.0 if bad_first else 1.0)).all()
+        if not bad_first:
+            assert (out[10:] == 5.0).all()
+
+
+def test_prefill_many_sequences():
+    """More sequences than a block has threads, most of one token."""
+    g = rng(12)
+    lens = [int(n) for n in torch.randint(0, 4, (1500,), generator=g)]
+    run_prefill(lens, lens, 2, 1, 64, True, 13)
+
+
+# ------------------------------------------------------------------ decode
+
+
+def run_decode(lens, nq, hq, hkv, dim, e4m3, page, seed, max_len=None, gain=1.5, poison=True, ws_extra=0):
+    g = rng(seed)
+    table, pages = R.make_table(g, lens, page)
+    kc, vc, ks, vs = R.make_cache(g, pages, hkv, page, dim, e4m3)
+    q = (torch.randn(len(lens) * nq, hq, dim, generator=g) * gain).bfloat16()
+    scale = dim ** -0.5
+    kd, vd, ksd, vsd = R.cuda(kc, vc, ks, vs)
+    if poison:   # rows past each sequence's end, and pages of no sequence
+        used = torch.zeros(pages, page, dtype=torch.bool)
+        for b, n in enumerate(lens):
+            j = torch.arange(n)
+            used[table[b].long()[j // page], j % page] = True
+        free = (~used)[:, None, :].expand(pages, hkv, page).cuda()
+        for t in (kd, vd):
+            if e4m3:
+                t.view(torch.uint8)[free] = 0x7F      # NaN
+            else:
+                t[free] = math.nan
+        for t in (ksd, vsd):
+            if t is not None:
+                t[free] = math.nan
+    c = m.attn_config(hq, hkv, dim, page, int(e4m3))
+    top = max(lens + [1]) if max_len is None else max_len
+    need = (top + page - 1) // page
+    if table.shape[1] < need:
+        table = torch.cat([table, torch.full((len(lens), need - table.shape[1]), -7, dtype=torch.int32)], 1)
+    ws = torch.full((m.attn_decode_workspace_size(c, len(lens), nq, top) + ws_extra,), 255, dtype=torch.uint8, device="cuda")
+    out = torch.full((len(lens) * nq, hq, dim), math.nan, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((len(lens) * nq, hq), math.nan, device="cuda")
+    err = err_word()
+    qd, tb, ln = R.cuda(q, table, torch.tensor(lens, dtype=torch.int32))
+    m.attn_decode(c, len(lens), nq, top, qd, hq * dim, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, scale, out, lse,
+                  ws, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    for b, n in enumerate(lens):
+        r = slice(b * nq, b * nq + nq)
+        ref = R.attend(q[r], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), scale,
+                       [max(0, n - nq + i + 1) for i in range(nq)])
+        R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens,nq,hq,hkv,page", [
+    ([1], 1, 1, 1, 16),
+    ([63, 64, 65], 1, 16, 2, 64),
+    ([0, 17, 1, 300], 1, 4, 4, 16),
+    ([1000], 1, 16, 2, 128),
+    ([5, 130, 1], 4, 16, 2, 32),          # verification rows; a sequence shorter than its new tokens
+    ([257, 700], 8, 8, 1, 64),            # 64 query rows of one key head
+    ([190], 3, 5, 1, 16),
+    ([2049, 31], 2, 12, 4, 32),
+    ([129], 8, 32, 2, 16),                # 128 query rows of one key head
+])
+def test_decode(lens, nq, hq, hkv, page, dim, e4m3):
+    run_decode(lens, nq, hq, hkv, dim, e4m3, page, seed=sum(lens) + dim)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_long_and_loose_bounds(e4m3):
+    run_decode([20000], 1, 16, 2, 128, e4m3, 64, 1)
+    run_decode([7, 20001, 5000], 2, 4, 1, 256, e4m3, 16, 2)
+    run_decode([7, 300], 1, 4, 2, 128, e4m3, 16, 3, max_len=100_000)      # max_len far above every length
+    run_decode([500], 1, 16, 2, 128, e4m3, 64, 4, gain=8.0)
+
+
+def test_decode_reports_bad_pages_and_lengths():
+    """A bad page reads as zeros (score 0, value 0) and is reported; so is a
+    length above max_len (cut) or below zero (none)."""
+    for e4m3 in (False, True):
+        g = rng(5)
+        table, pages = R.make_table(g, [40, 40], 16)
+        kc, vc, ks, vs = R.make_cache(g, pages, 1, 16, 64, e4m3)
+        c = m.attn_config(2, 1, 64, 16, int(e4m3))
+        q = torch.randn(2, 2, 64, generator=g).bfloat16()
+        good = table.clone()
+        table[0, 1], table[1, 2] = pages, -1
+        ws = torch.zeros(m.attn_decode_workspace_size(c, 2, 1, 48), dtype=torch.uint8, device="cuda")
+        for tb, lens, cut in ((table, [40, 40], [40, 40]), (good, [60, -3], [48, 0])):
+            out = torch.empty(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+            err = err_word()
+            m.attn_decode(c, 2, 1, 48, q.cuda(), 128, tb.cuda(), 3, torch.tensor(lens, dtype=torch.int32).cuda(),
+                          pages, *R.cuda(kc, vc, ks, vs), 0.125, out, None, ws, err=err)
+            torch.cuda.synchronize()
+            assert err.item() == m.MOE_ERR_BOUNDS
+            for b in range(2):
+                bad = (tb[b] < 0) | (tb[b] >= pages)
+                k, v = (R.rows_of(x, s, torch.where(bad, 0, tb[b]), cut[b]) for x, s in ((kc, ks), (vc, vs)))
+                gone = bad[torch.arange(cut[b]) // 16]
+                k[gone], v[gone] = 0, 0
+                R.check_attention(out[b:b + 1].cpu(), None, R.attend(q[b:b + 1], k, v, 0.125, [cut[b]]))
+
+
+def test_decode_non_finite_row_reaches_its_own_sequence_only():
+    g = rng(6)
+    table, pages = R.make_table(g, [100, 100], 32)
+    kc, vc, ks, vs = R.make_cache(g, pages, 1, 32, 128, True)
+    ks[table[0, 1].long(), 0, 3] = math.nan
+    c = m.attn_config(4, 1, 128, 32, 1)
+    q = torch.randn(2, 4, 128, generator=g).bfloat16()
+    ws = torch.zeros(m.attn_decode_workspace_size(c, 2, 1, 100), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    m.attn_decode(c, 2, 1, 100, q.cuda(), 512, table.cuda(), table.stride(0), torch.tensor([100, 100]).int().cuda(),
+                  pages, *R.cuda(kc, vc, ks, vs), 0.1, out, None, ws)
+    torch.cuda.synchronize()
+    assert out[0].isnan().all() and out[1].isfinite().all()
+
+
+# ------------------------------------------------------------------ a layer's run
+
+
+def layer_case(e4m3, dim=128, hq=16, hkv=2, page=32, pages=64):
+    g = rng(21)
+    inv = torch.pow(10000.0, -torch.arange(0, 64, 2).double() / 64).float()
+    qw, kw = ((1 + 0.2 * torch.randn(dim, generator=g)).bfloat16() for _ in range(2))
+    L = m.AttentionLayer(hq, hkv, dim, pages, page_size=page, cache_type=int(e4m3), q_weight=qw, k_weight=kw,
+                         inv_freq=inv)
+    return g, L, qw, kw, inv
+
+
+def layer_reference(g, L, qkv, qw, kw, inv, pos, e4m3, exact_tail=0):
+    """q, and k and v as the cache holds them (the last exact_tail rows as they
+    came), of one sequence."""
+    c = L.cfg
+    (q, _), (k, _), v = R.prepared(qkv, c.q_heads, c.kv_heads, c.head_dim, qw, kw, L.eps, inv, 64, 0, 1.0, pos)
+    q, k, v = q.bfloat16(), k.float(), v.float()
+    if e4m3:
+        k, v = ((x.float() * s[..., None]) for x, s in (R.quantised(k), R.quantised(v)))
+    return q, k, v
+
+
+@pytest.mark.parametrize("e4m3,dim", [(False, 128), (True, 128), (True, 256), (False, 64)])
+def test_layer_prompt_chunk_and_steps(e4m3, dim):
+    """A prompt, a second chunk after it (read back from the cache), then
+    verification rows and single tokens, as a server runs them, of two
+    sequences; every output against the whole sequence in 64 bits.  The bound
+    adds what rounding q and k once more (bf16) and 8-bit codes that fall to
+    the other side of a border may move: 3 % of the largest output."""
+    g, L, qw, kw, inv = layer_case(e4m3, dim)
+    page, lens = L.cfg.page_size, [200, 77]
+    total = 330
+    qkv = [torch.randn(total, L.row, generator=g).bfloat16() for _ in lens]
+    table = torch.randperm(L.num_pages, generator=g)[:22].view(2, 11).int()
+    at = [0, 0]
+    got = [[], []]
+
+    def step(counts, fn):
+        rows = torch.cat([qkv[b][at[b]:at[b] + n] for b, n in enumerate(counts)]).cuda()
+        pos = torch.cat([torch.arange(at[b], at[b] + n) for b, n in enumerate(counts)])
+        slots = torch.cat([table[b].long()[torch.arange(at[b], at[b] + n) // page] * page +
+                           torch.arange(at[b], at[b] + n) % page for b, n in enumerate(counts)])
+        for b, n in enumerate(counts):
+            at[b] += n
+        out = fn(rows, pos.int().cuda(), slots.int().cuda())
+        L.check()
+        for b, o in enumerate(out.cpu().split(counts)):
+            got[b].append(o)
+
+    step(lens, lambda r, p, s: L.prefill(r, p, s, R.starts(lens).cuda()))
+    step([60, 100], lambda r, p, s: L.prefill(r, p, s, R.starts([60, 100]).cuda(), table.cuda(),
+                                              R.starts(at).cuda(), sum(at)))
+    for nq in (1, 4, 1):
+        step([nq, nq], lambda r, p, s: L.decode(r, p, s, table.cuda(), torch.tensor(at).int().cuda(), 352))
+    for b in range(2):
+        n = at[b]
+        out = torch.cat(got[b]).double()
+        q, k, v = layer_reference(g, L, qkv[b][:n], qw, kw, inv, torch.arange(n), e4m3)
+        o, _, _, _ = R.attend(q, k, v, L.scale, [i + 1 for i in range(n)])
+        if e4m3:   # the first prompt saw its own keys before they were rounded to 8 bits
+            qe, ke, ve = layer_reference(g, L, qkv[b][:lens[b]], qw, kw, inv, torch.arange(lens[b]), False)
+            o[:lens[b]] = R.attend(qe, ke, ve, L.scale, [i + 1 for i in range(lens[b])])[0]
+        assert (out - o).abs().max() <= 0.03 * o.abs().max()
+
+
+def test_layer_decode_captured_and_replayed():
+    """The decode calls in a CUDA graph, replayed with new inputs and lengths,
+    equal the calls outside it; two graphs in flight on two streams too."""
+    g, L, qw, kw, inv = layer_case(True)
+    page = L.cfg.page_size
+    table = torch.randperm(L.num_pages, generator=g)[:20].view(2, 10).int().cuda()
+    L.k_cache.copy_(torch.randn(L.k_cache.shape, generator=g).to(torch.float8_e4m3fn))
+    L.v_cache.copy_(torch.randn(L.v_cache.shape, generator=g).to(torch.float8_e4m3fn))
+    qkv = torch.randn(2, L.row, generator=g).bfloat16().cuda()
+    lens = torch.tensor([100, 250], dtype=torch.int32).cuda()
+
+    def slots():
+        p = lens.long() - 1
+        return (table.long().gather(1, (p // page)[:, None])[:, 0] * page + p % page).int()
+
+    pos, sl = lens - 1, slots()
+    graphs = []
+    for _ in range(2):
+        L.decode(qkv, pos, sl, table, lens, 320)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = L.decode(qkv, pos, sl, table, lens, 320)
+        graphs.append((gr, out))
+    for n in ((100, 250), (1, 320), (64, 65)):
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        pos.copy_(lens - 1)
+        sl.copy_(slots())
+        qkv.copy_(torch.randn(2, L.row, generator=g).bfloat16())
+        want = L.decode(qkv, pos, sl, table, lens, 320).clone()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for (gr, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+                gr.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out, want)
+    L.check()
+
+
+def test_layer_refusals():
+    _, L, *_ = layer_case(False)
+    z = lambda *s, **kw: torch.zeros(*s, **{**dict(dtype=torch.int32, device="cuda"), **kw})  # noqa: E731
+    rows = z(4, L.row, dtype=torch.bfloat16)
+    ok = (rows, z(4), z(4) - 1)
+    with pytest.raises(TypeError, match="qkv"):
+        L.prefill(rows.float(), z(4), z(4), z(2))
+    with pytest.raises(ValueError, match="qkv must have shape"):
+        L.prefill(rows[:, 8:], z(4), z(4), z(2))
+    with pytest.raises(ValueError, match="slots must have shape"):
+        L.prefill(rows, z(4), z(3), z(2))
+    with pytest.raises(ValueError, match="positions is on cpu"):
+        L.prefill(rows, z(4).cpu(), z(4), z(2))
+    with pytest.raises(TypeError, match="cu_q"):
+        L.prefill(*ok, z(2).long())
+    with pytest.raises(ValueError, match="total_k"):
+        L.prefill(*ok, z(2), z(1, 4), z(2))
+    with pytest.raises(ValueError, match="3 sequences"):
+        L.decode(*ok, z(3, 4), z(3), 10)
+    with pytest.raises(ValueError, match="page_table rows"):
+        L.decode(*ok, z(4, 1), z(4), 100)
+    with pytest.raises(ValueError, match="no rows"):
+        L.prefill(rows[:0], z(0), z(0), z(2))
+    L.decode(rows, z(4), z(4) + L.num_pages * 32, z(4, 1), z(4) + 1, 32)
+    with pytest.raises(m.MoeError, match="MOE_ERR_BOUNDS"):
+        L.check()
+    L.check()
