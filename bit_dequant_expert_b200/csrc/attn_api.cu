@@ -32,7 +32,7 @@ int32_t check_cache(const attn_config_t* c, int32_t num_pages, const void* k, co
     if (num_pages < 1 || !k || !v || !aligned(k, 16) || !aligned(v, 16)) return MOE_ERR_INVALID_ARG;
     if (c->cache_type == ATTN_CACHE_E4M3 && (!ks || !vs || !aligned(ks, 16) || !aligned(vs, 16)))
         return MOE_ERR_INVALID_ARG;
-    if ((int64_t)num_pages * c->page_size * c->kv_heads > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)num_pages * c->page_size * c->kv_heads > 0x7FFFFF00) return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

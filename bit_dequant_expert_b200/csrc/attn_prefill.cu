@@ -143,12 +143,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, 
     return true;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // O row (D columns from taddr of this thread's lane) times f.
 template <int D>
 __device__ __forceinline__ void rescale_row(uint32_t taddr, float f) {
