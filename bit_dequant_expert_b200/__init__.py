@@ -14,6 +14,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 
@@ -150,11 +152,27 @@ def _nbytes(t) -> int:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_device() -> int:
+    return torch.cuda.current_device()
+
+
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# torch's own direct reads of the current device and stream, several microseconds shorter than the calls above
+if hasattr(torch._C, "_cuda_getDevice") and hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _current_device() -> int:   # noqa: F811
+        torch.cuda._lazy_init()
+        return torch._C._cuda_getDevice()
+
+    _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(status: int, call: str, raise_on_error: bool) -> int:
@@ -241,28 +259,39 @@ def gdn_scan(B, T, Hk, Hv, dk, dv, q, k, v, g, beta, scale, state_in, state_out,
     return _check(st, "gdn_scan", raise_on_error)
 
 
-def _dptr(t, name: str, dtypes: tuple, rows: bool = False) -> int | None:
-    """_ptr of a tensor on the GPU, of one of these types and contiguous (rows:
-    contiguous within its first dimension's rows)."""
-    if t is None or isinstance(t, int):
-        return t
+def _bad_tensor(t, name: str, kind) -> None:
     if not t.is_cuda:
         raise ValueError("%s is on %s, not on a GPU" % (name, t.device))
-    if str(t.dtype)[6:] not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(dtypes), t.dtype))
-    if not t.is_contiguous() and not (rows and t.numel() and t[0].is_contiguous()):
-        raise ValueError("%s must be contiguous" % name)
+    if t.dtype is not kind:
+        raise TypeError("%s must be %s, got %s" % (name, kind, t.dtype))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _dptr(t, name: str, kind) -> int | None:
+    """_ptr of a contiguous tensor of type `kind` on the GPU."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not kind or not t.is_cuda or not t.is_contiguous():
+        _bad_tensor(t, name, kind)
     return t.data_ptr()
 
 
-_BF16 = ("bfloat16",)
-_FP32 = ("float32",)
-_INT32 = ("int32",)
-_CACHE = {ATTN_CACHE_BF16: ("bfloat16",), ATTN_CACHE_E4M3: ("float8_e4m3fn", "uint8")}
+def _rptr(t, name: str, kind) -> int | None:
+    """_ptr of a tensor of type `kind` on the GPU whose rows (along the first dimension) are contiguous."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not kind or not t.is_cuda or not (t.is_contiguous() or (t.numel() and t[0].is_contiguous())):
+        _bad_tensor(t, name, kind)
+    return t.data_ptr()
+
+
+_BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def _cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale) -> tuple:
-    kind = _CACHE.get(cfg.cache_type, ())
+    kind = _BF16
+    if cfg.cache_type == ATTN_CACHE_E4M3:   # codes may come as bytes
+        kind = torch.uint8 if getattr(k_cache, "dtype", None) is torch.uint8 else torch.float8_e4m3fn
     return (_dptr(k_cache, "k_cache", kind), _dptr(v_cache, "v_cache", kind), _dptr(k_scale, "k_scale", _FP32),
             _dptr(v_scale, "v_scale", _FP32))
 
@@ -271,7 +300,7 @@ def attn_qkv_prepare(cfg, T, qkv, qkv_stride, q_weight, k_weight, eps, inv_freq,
                      positions, slots, num_pages, k_cache, v_cache, k_scale, v_scale, q_out, k_out, err=None,
                      stream=None, raise_on_error=True) -> int:
     """Norm of queries and keys, rotation of their positions, cache write (include/attn_b200.h)."""
-    st = _lib.attn_qkv_prepare(ctypes.byref(cfg), T, _dptr(qkv, "qkv", _BF16, True), qkv_stride,
+    st = _lib.attn_qkv_prepare(ctypes.byref(cfg), T, _rptr(qkv, "qkv", _BF16), qkv_stride,
                                _dptr(q_weight, "q_weight", _BF16), _dptr(k_weight, "k_weight", _BF16), eps,
                                _dptr(inv_freq, "inv_freq", _FP32), rot_dim, rope_layout, rope_scale,
                                _dptr(positions, "positions", _INT32), _dptr(slots, "slots", _INT32), num_pages,
@@ -283,7 +312,7 @@ def attn_qkv_prepare(cfg, T, qkv, qkv_stride, q_weight, k_weight, eps, inv_freq,
 def attn_kv_read(cfg, B, total, page_table, page_table_stride, cu_lens, num_pages, k_cache, v_cache, k_scale, v_scale,
                  k_out, v_out, err=None, stream=None, raise_on_error=True) -> int:
     """The cache's rows of each sequence, packed, in bf16 (include/attn_b200.h)."""
-    st = _lib.attn_kv_read(ctypes.byref(cfg), B, total, _dptr(page_table, "page_table", _INT32, True),
+    st = _lib.attn_kv_read(ctypes.byref(cfg), B, total, _rptr(page_table, "page_table", _INT32),
                            page_table_stride, _dptr(cu_lens, "cu_lens", _INT32), num_pages,
                            *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), _dptr(k_out, "k_out", _BF16),
                            _dptr(v_out, "v_out", _BF16), _dptr(err, "err", _INT32), _stream(stream))
@@ -294,8 +323,8 @@ def attn_prefill(cfg, B, total_q, total_k, cu_q, cu_k, q, q_stride, k, k_stride,
                  lse=None, err=None, stream=None, raise_on_error=True) -> int:
     """Attention over packed prompts (include/attn_b200.h)."""
     st = _lib.attn_prefill(ctypes.byref(cfg), B, total_q, total_k, _dptr(cu_q, "cu_q", _INT32),
-                           _dptr(cu_k, "cu_k", _INT32), _dptr(q, "q", _BF16, True), q_stride, _dptr(k, "k", _BF16, True),
-                           k_stride, _dptr(v, "v", _BF16, True), v_stride, scale, int(causal), _dptr(out, "out", _BF16),
+                           _dptr(cu_k, "cu_k", _INT32), _rptr(q, "q", _BF16), q_stride, _rptr(k, "k", _BF16),
+                           k_stride, _rptr(v, "v", _BF16), v_stride, scale, int(causal), _dptr(out, "out", _BF16),
                            _dptr(lse, "lse", _FP32), _dptr(err, "err", _INT32), _stream(stream))
     return _check(st, "attn_prefill", raise_on_error)
 
@@ -309,11 +338,12 @@ def attn_decode(cfg, B, nq, max_len, q, q_stride, page_table, page_table_stride,
                 raise_on_error=True) -> int:
     """Attention of a few new tokens per sequence over the cache (include/attn_b200.h)."""
     n = _nbytes(ws) if ws_bytes is None else ws_bytes
-    st = _lib.attn_decode(ctypes.byref(cfg), B, nq, max_len, _dptr(q, "q", _BF16, True), q_stride,
-                          _dptr(page_table, "page_table", _INT32, True), page_table_stride,
+    st = _lib.attn_decode(ctypes.byref(cfg), B, nq, max_len, _rptr(q, "q", _BF16), q_stride,
+                          _rptr(page_table, "page_table", _INT32), page_table_stride,
                           _dptr(seq_lens, "seq_lens", _INT32), num_pages,
                           *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), scale, _dptr(out, "out", _BF16),
-                          _dptr(lse, "lse", _FP32), _ptr(ws), n, _dptr(err, "err", _INT32), _stream(stream))
+                          _dptr(lse, "lse", _FP32), _dptr(ws, "ws", torch.uint8), n, _dptr(err, "err", _INT32),
+                          _stream(stream))
     return _check(st, "attn_decode", raise_on_error)
 
 

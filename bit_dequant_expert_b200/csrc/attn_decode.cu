@@ -2,22 +2,28 @@
 // the bytes of the cache, each read once.
 //
 // The nq G query rows (nq tokens, G heads) of a key/value head share its keys:
-// they are the rows of m16n8k16 products, 16, 32 or 64 to a block.  A block
-// takes one chunk of a sequence's keys for one key/value head, 64 keys a
-// tile; TMA brings K and V pages (and scales) into a ring of swizzled tiles,
-// so that the loads of several tiles are in flight while one is worked on.
-// Each warp keeps the running maximum m, sum l and output O of its 16 rows
-// over its share of each tile's keys (no exchange inside the loop); at the
-// end the shares are joined in shared memory.  A sequence of one chunk is
-// finished there; the chunks of a longer one leave (O, m, l) in the workspace
-// for k_attn_combine.
+// they are the rows of m16n8k16 products.  The keys of all sequences and heads
+// are cut into tiles of 64, and one resident block a multiprocessor takes an
+// equal run of the whole list of tiles, whatever the sequences' lengths: a
+// producer warp keeps a ring of TMA page loads (K, V and scales, swizzled)
+// full across the ends of sequences, two groups of four warps take alternate
+// tiles.  Each warp keeps the running maximum m, sum l and output O of its
+// rows over its share of the tiles' keys (no exchange inside the loop); where
+// the run leaves a sequence's head, the shares are joined in shared memory.  A
+// head that one block did whole is finished there; of one cut at a run's end
+// (O, m, l) go to the workspace for k_attn_combine.
 //
-// 8-bit cache: e4m3 codes become bf16 exactly, four bytes of a register to
-// two pairs (the shift puts the exponent in place, a product with 2^120
-// corrects its bias and subnormals), with no shuffles: the queries are laid
-// out for the order in which the bytes come, and a transposed load of byte
-// pairs gives the even and the odd elements of V as two column tiles.  A key's
-// scale multiplies its score, a value's its probability.
+// 8-bit cache: the products run in f16, which holds every e4m3 code exactly;
+// a register of four codes becomes two pairs by two conversions, with no
+// shuffles: the queries are laid out for the order in which the bytes come,
+// and a transposed load of byte pairs gives the even and the odd elements of
+// V as two column tiles.  A query row is brought to a largest magnitude in
+// [1, 2) by a power of two (exact: bf16 has fewer bits; what falls below
+// 2^-24 of the row's largest is under the sums' own rounding), a key's scale
+// multiplies its score, a value's its probability.  The running maximum m is
+// that of score + log2 of the value's scale, so that a probability times its
+// scale, p = exp2(s - m) vs, stays at most 2^8 and the largest near 1: it is
+// rounded to f16, 2^-11 of itself or 2^-25 of the largest.
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -33,47 +39,75 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 64;            // keys of a tile
-constexpr int kMaxChunk = 8192;      // keys of a chunk at most (bounds the page list)
 constexpr int kSms = 148;
+constexpr int kThreads = 384;        // two groups of consumers, a third of which one warp loads
+constexpr int kConsumers = 256;
+// Registers a thread: all start with 168; the third group gives its own up to the others: 2 * 224 + 56 = 3 * 168.
+constexpr int kRegsConsumer = 224, kRegsProducer = 56;
+constexpr int kMinTiles = 2;         // tiles of a run at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLeast = -100.0f;    // log2 of the least value scale the running maximum follows
 constexpr float kGrow = 8.0f;        // log2 of the growth of a row's maximum that O is rescaled for
 
-// Row tiles a block holds: 16 rows each.
-int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Tiles of 16 query rows that a block works on at once (more rows take more passes over the keys).
+int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : rows <= 32 || dim == 256 ? 2 : 4; }
 
 template <int D, bool kE4m3, int MT>
 struct Cfg {
-    static constexpr int kWarps = MT == 1 ? 4 : 8;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kSplits = kWarps / MT;              // shares of a tile's keys
+    // Row tiles of one warp: two where its outputs fit the registers, so that a key's fragments (and their
+    // conversions) serve 32 rows; the sets of warps of a group that share out the row tiles
+    static constexpr int kRT = MT == 1 || D == 256 ? 1 : 2;
+    static constexpr int kSets = MT / kRT;
+    static constexpr int kSplits = 4 / kSets;                // shares of a tile's keys
     static constexpr int kKeys = kTile / kSplits;            // keys of a share: 16 or 32
+    static constexpr int kShares = 2 * kSplits;              // of a row tile, both groups
     static constexpr int kRow = D * (kE4m3 ? 1 : 2);         // bytes of a cache row
     static constexpr int kBlock = kRow < 128 ? kRow : 128;   // swizzled bytes of a row's blocks
     static constexpr int kStage = 2 * kTile * kRow;          // K and V of a tile
-    // two blocks an SM where a third of half its memory holds a tile, else one; as many stages as fit beside the queries
-    static constexpr int kBlocks = MT == 1 && kStage <= 33 * 1024 ? 2 : 1;
-    static constexpr int kBytes = (kBlocks == 2 ? 112 : 226) * 1024 - 16 * MT * D * 2 - 5 * 1024;
-    static constexpr int kStages = kBytes / (kStage + 1024) > 8 ? 8 : kBytes / (kStage + 1024);
-    static constexpr bool kQRegs = D <= 128;                 // query fragments in registers
+    static constexpr int kPad = kE4m3 ? 16 : 8;              // floats between output rows: no bank conflicts
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kRest = kRows * (D * 2 + (D + kPad) * 4 + kShares * 8 + 16) + 1024;
+    static constexpr int kFit = (226 * 1024 - kRest) / (kStage + kTile * 8 + 16);
+    static constexpr int kStages = kFit > 12 ? 12 : kFit;
+    static constexpr bool kQRegs = D <= 128 && kRT == 1;     // query fragments in registers
 };
 
 template <int D, bool kE4m3, int MT>
 struct Smem {
     using C = Cfg<D, kE4m3, MT>;
-    uint8_t kv[C::kStages][C::kStage];                       // 1024-aligned; at the end the shares' outputs
-    uint8_t q[16 * MT * D * 2];
+    uint8_t kv[C::kStages][C::kStage];                       // 1024-aligned
+    uint8_t q[C::kRows * D * 2];
+    float acc[C::kRows][D + C::kPad];
     float scale[C::kStages][kE4m3 ? 2 * kTile : 4];          // K's, then V's
     uint64_t full[C::kStages], empty[C::kStages];
-    float ml[C::kWarps][16][2];
-    int pages[kMaxChunk / 16];
+    float ml[C::kShares][C::kRows][2];
+    float fin[C::kRows][2];
+    float q_scale[C::kRows];
+    long long scan[14];
+    int find;
     int dead;
 };
 
 struct DecodeGrid {
-    int chunk, chunks;               // keys of a chunk, chunks of max_len keys
-    int rows, row_blocks;            // query rows of a key/value head, blocks of 16 MT of them
+    int blocks;                      // blocks launched
+    int page_shift;                  // log2 of page_size
+    int rows, row_blocks;            // query rows of a key/value head, passes of 16 MT of them
+    int units;                       // heads x passes of a sequence
+    int row_pad;                     // 16 MT
+    int64_t out_at;                  // workspace: tiles before each sequence (int64 [B + 1]), then partial outputs,
+    int64_t ml_at;                   // then their maxima and sums (byte offsets)
 };
+
+// Tiles of a sequence's unit; an empty one has a tile without keys, which writes its zeros.
+__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
+__device__ __forceinline__ int clamp_len(int len, int max_len) { return len < 0 ? 0 : min(len, max_len); }
+
+// Runs: block i of n takes tiles [total i / n, total (i + 1) / n).
+__device__ __forceinline__ long long run_start(long long total, int i, int n) { return total * i / n; }
+__device__ __forceinline__ int runs_of(long long total, int blocks) {
+    return (int)min((long long)blocks, max(1ll, total / kMinTiles));
+}
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* err) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -89,24 +123,39 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, 
     return true;
 }
 
-// Bytes 0 and 2 (even) or 1 and 3 (odd) of w, e4m3, as a bf16 pair: sign,
-// exponent and mantissa move to their places, which reads 2^-120 of the value
-// (bias 7 against 127; subnormals included), and a product with 2^120 puts it
-// right.  Exact for every finite code.
-__device__ __forceinline__ uint32_t scale_up(uint32_t v) {
+// Codes 0 and 1 (lo) or 2 and 3 (hi) of w as an f16 pair (exact).
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(0x7B807B80u));
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(d) : "r"(w));
     return d;
 }
-__device__ __forceinline__ uint32_t e4m3_even(uint32_t w) {
-    return scale_up(((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u));
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
+    uint32_t d;
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(d) : "r"(w));
+    return d;
 }
-__device__ __forceinline__ uint32_t e4m3_odd(uint32_t w) {
-    return scale_up(((w >> 4) & 0x07F007F0u) | (w & 0x80008000u));
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two bf16 elements times f, as an f16 pair.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) { return pack_f16x2(bf16_lo(w) * f, bf16_hi(w) * f); }
+
+// The second product's rounding of a probability pair.
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi) { return kE4m3 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); }
+
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 template <int D, bool kE4m3, int MT>
-__global__ void __launch_bounds__(Cfg<D, kE4m3, MT>::kThreads, Cfg<D, kE4m3, MT>::kBlocks)
+__global__ void __launch_bounds__(kThreads, 1)
     k_attn_decode(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const AttnDecodeArgs a, const DecodeGrid g) {
     using C = Cfg<D, kE4m3, MT>;
@@ -114,457 +163,605 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, MT>::kThreads, Cfg<D, kE4m3, MT>
     Smem<D, kE4m3, MT>& sm =
         *reinterpret_cast<Smem<D, kE4m3, MT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, P = a.c.page_size;
-    const int b = blockIdx.z, kvh = blockIdx.y / g.row_blocks, row0 = blockIdx.y % g.row_blocks * (16 * MT);
-    const int rows = min(16 * MT, g.rows - row0);
-
-    griddep_launch_dependents();
-    griddep_wait();
-    int len = a.lens[b];
-    if (len < 0 || len > a.max_len) {
-        if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_error(a.err, MOE_ERR_BOUNDS);
-        len = len < 0 ? 0 : a.max_len;
-    }
-    const int k0 = blockIdx.x * g.chunk;
-    if (k0 >= len && blockIdx.x > 0) return;
-    const int n = min(g.chunk, len - k0);                    // keys of this chunk (0: an empty sequence)
-    const int ntiles = (n + kTile - 1) / kTile;
+    const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, ps = g.page_shift;
+    const int ss = min(ps, 6), sub = 1 << ss, nsub = kTile >> ss;   // rows of a TMA box, boxes of a tile
+    long long* prefix = reinterpret_cast<long long*>(a.ws);
 
     if (tid == 0) {
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sm.full[i], 1);
-            mbar_init(&sm.empty[i], C::kWarps);
+            mbar_init(&sm.empty[i], 4);
         }
         sm.dead = 0;
         fence_mbar_init();
     }
-    // the chunk's pages: row of the caches at which this head's page begins, -1 for a bad one
-    const int p0 = k0 / P, np = n > 0 ? (k0 + n - 1) / P - p0 + 1 : 0;
-    for (int i = tid; i < np; i += C::kThreads) {
-        const int page = a.page_table[b * a.table_stride + p0 + i];
-        const bool in = page >= 0 && page < a.cache.num_pages;
-        if (!in) set_error(a.err, MOE_ERR_BOUNDS);
-        sm.pages[i] = in ? (page * Hk + kvh) * P : -1;
-    }
-    // the query rows, 16-byte pieces swizzled by row; for the 8-bit cache each 16 elements in the order
-    // 0 2 4 6 .. within their quads (even, then odd), as the keys' bytes come
-    for (int i = tid; i < 16 * MT * (D / 16); i += C::kThreads) {
-        const int r = i / (D / 16), c = i % (D / 16);
-        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-        if (r < rows) {
-            const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
-            x = src[2 * c];
-            y = src[2 * c + 1];
-        }
-        if (kE4m3) {
-            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-            x = make_uint4(prmt(w[0], w[1], 0x5410), prmt(w[2], w[3], 0x5410), prmt(w[4], w[5], 0x5410),
-                           prmt(w[6], w[7], 0x5410));
-            y = make_uint4(prmt(w[0], w[1], 0x7632), prmt(w[2], w[3], 0x7632), prmt(w[4], w[5], 0x7632),
-                           prmt(w[6], w[7], 0x7632));
-        }
-        uint8_t* dst = sm.q + r * (D * 2);
-        *reinterpret_cast<uint4*>(dst + ((2 * c) ^ (r & 7)) * 16) = x;
-        *reinterpret_cast<uint4*>(dst + ((2 * c + 1) ^ (r & 7)) * 16) = y;
-    }
-    __syncthreads();
+    griddep_launch_dependents();
+    griddep_wait();
 
-    const int mt = warp % MT, split = warp / MT;
-    const int sub = min(P, kTile), nsub = kTile / sub;       // rows of a TMA box, boxes of a tile
-    // One warp brings tile t: its lanes take a box each.
-    auto load_tile = [&](int t) {
-        const int st = t % C::kStages;
-        const int key = t * kTile + lane * sub;              // within the chunk
-        int row = -1;
-        bool in = lane < nsub && key < n;
-        if (in) {
-            row = sm.pages[(k0 + key) / P - p0];
-            if (row >= 0) row += (k0 + key) % P;
+    // ---- the run: where it begins in the list of (sequence, head and pass, tile)
+    long long total = 0, first_before = 0;
+    int first_n = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + tid;
+        int n = 0;
+        if (b < a.B) {
+            const int len = a.lens[b];
+            if ((len < 0 || len > a.max_len) && blockIdx.x == 0) set_error(a.err, MOE_ERR_BOUNDS);
+            n = tiles_of(clamp_len(len, a.max_len));
         }
-        if (kE4m3 && in && row < 0)                          // a bad page: zeros from outside the map, scales zero
-            for (int i = 0; i < sub; ++i) sm.scale[st][lane * sub + i] = sm.scale[st][kTile + lane * sub + i] = 0.0f;
-        const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, in));
-        const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, in && row >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], boxes * sub * C::kRow * 2 + (kE4m3 ? scaled * sub * 8 : 0));
-        __syncwarp();
-        if (in) {
-            const int at = row >= 0 ? row : a.cache.num_pages * Hk * P;
-            uint8_t* dst = sm.kv[st] + lane * sub * C::kRow;
-            tma_load_3d(dst, &k_map, 0, at, 0, &sm.full[st]);
-            tma_load_3d(dst + kTile * C::kRow, &v_map, 0, at, 0, &sm.full[st]);
-            if (kE4m3 && row >= 0) {
-                bulk_load(&sm.scale[st][lane * sub], a.cache.ks + row, sub * 4, &sm.full[st]);
-                bulk_load(&sm.scale[st][kTile + lane * sub], a.cache.vs + row, sub * 4, &sm.full[st]);
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) sm.scan[warp] = inc;
+        __syncthreads();
+        long long before = total + inc - n;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sm.scan[w];
+            total += sm.scan[w];
+        }
+        if (b < a.B && blockIdx.x == 0) prefix[b] = before;
+        if (base == 0) first_before = before, first_n = n;
+        __syncthreads();
+    }
+    if (tid == 0 && blockIdx.x == 0) prefix[a.B] = total;
+    const int U = g.units;
+    total *= U;
+    const int runs = runs_of(total, gridDim.x);
+    if ((int)blockIdx.x >= runs) return;
+    const long long start = run_start(total, blockIdx.x, runs), end = run_start(total, blockIdx.x + 1, runs);
+    {
+        const long long at = start / U;
+        if (tid < a.B && at >= first_before && at < first_before + first_n) {
+            sm.find = tid;
+            sm.scan[12] = first_before;
+        }
+        // more sequences than threads: later ones by another pass over their lengths
+        long long before0 = 0;
+        for (int base = 0; a.B > kThreads && base < a.B; base += kThreads) {
+            const int b = base + tid;
+            const int n = b < a.B ? tiles_of(clamp_len(a.lens[b], a.max_len)) : 0;
+            long long inc = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) sm.scan[warp] = inc;
+            __syncthreads();
+            long long before = before0 + inc - n;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += sm.scan[w];
+                before0 += sm.scan[w];
+            }
+            __syncthreads();
+            if (n > 0 && at >= before && at < before + n) {
+                sm.find = b;
+                sm.scan[12] = before;
             }
         }
-    };
-    if (warp == 0)
-        for (int t = 0; t < min(ntiles, C::kStages); ++t) load_tile(t);
-
-    // fragments of the 16 query rows
-    const uint32_t q_saddr = smem_u32(sm.q) + (mt * 16 + (lane & 15)) * (D * 2);
-    const int q_swz = lane & 7, q_hi = lane >> 4;
-    uint32_t qf[C::kQRegs ? D / 16 : 1][4];
-    if (C::kQRegs) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) ldmatrix4(q_saddr + ((2 * k + q_hi) ^ q_swz) * 16, qf[k]);
+        __syncthreads();
     }
+    int b = sm.find, len = clamp_len(a.lens[b], a.max_len), nt = tiles_of(len);
+    const long long rem = start - sm.scan[12] * U;
+    int u = (int)(rem / nt), tile = (int)(rem % nt);
+    int left = (int)(end - start), it = 0;                   // tiles of the run to go, and done
 
-    // addresses of this lane's rows within a tile: K's (blocks of 8 keys in lanes 0-15 and 16-31) and V's
-    // (in lanes 0-7 and 8-15), per 16 keys of the share
-    constexpr int kSteps = C::kKeys / 16;
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+        // ------------------------------------------------------ loads: the lanes of warp 8 take a box of a tile each
+        if (warp == 8) {
+            bool ok = true;
+            auto page_at = [&]() {                           // of this lane's box of the tile; -2: past the end
+                const int key = tile * kTile + (lane << ss);
+                return lane < nsub && key < len ? max(a.page_table[b * a.table_stride + (key >> ps)], -1) : -2;
+            };
+            int page = page_at();
+            while (left > 0) {
+                const int st = it % C::kStages, kvh = u / g.row_blocks;
+                const bool in = page != -2, good = in && page >= 0 && page < a.cache.num_pages;
+                if (in && !good) set_error(a.err, MOE_ERR_BOUNDS);
+                // a bad page reads as zeros, from outside the map
+                const int row = good ? ((page * Hk + kvh) << ps) + ((tile * kTile + (lane << ss)) & ((1 << ps) - 1))
+                                     : (a.cache.num_pages * Hk) << ps;
+                ++it, --left;
+                if (++tile == nt) {
+                    tile = 0;
+                    if (++u == U && left > 0) {
+                        u = 0, ++b;
+                        len = clamp_len(a.lens[b], a.max_len);
+                        nt = tiles_of(len);
+                    }
+                }
+                if (left > 0) page = page_at();              // on its way while this tile waits for its place
+                if (it > C::kStages) {
+                    ok = wait(&sm.empty[st], ((it - 1) / C::kStages - 1) & 1, &sm.dead, a.err);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                }
+                if (kE4m3 && in && !good)
+                    for (int i = 0; i < sub; ++i)
+                        sm.scale[st][(lane << ss) + i] = sm.scale[st][kTile + (lane << ss) + i] = 0.0f;
+                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, in));
+                const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm.full[st], boxes * sub * C::kRow * 2 + (kE4m3 ? scaled * sub * 8 : 0));
+                __syncwarp();
+                if (in) {
+                    uint8_t* dst = sm.kv[st] + (lane << ss) * C::kRow;
+                    tma_load_3d(dst, &k_map, 0, row, 0, &sm.full[st]);
+                    tma_load_3d(dst + kTile * C::kRow, &v_map, 0, row, 0, &sm.full[st]);
+                    if (kE4m3 && good) {
+                        bulk_load(&sm.scale[st][lane << ss], a.cache.ks + row, sub * 4, &sm.full[st]);
+                        bulk_load(&sm.scale[st][kTile + (lane << ss)], a.cache.vs + row, sub * 4, &sm.full[st]);
+                    }
+                }
+            }
+            if (!ok)                                         // leave no copy in flight behind
+                for (int i = max(0, it - 1 - C::kStages); i < it - 1; ++i)
+                    mbar_wait_bounded(&sm.full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+        }
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
+    // ---------------------------------------------------------- products
+    constexpr int RT = C::kRT;
+    const int wg = warp >> 2, set = (warp & 3) % C::kSets, split = (warp & 3) / C::kSets;
+    const int share = wg * C::kSplits + split;
+
+    // fragments of the warp's query rows
+    const uint32_t q_saddr = smem_u32(sm.q) + (set * RT * 16 + (lane & 15)) * (D * 2);
+    const int q_swz = lane & 7, q_hi = lane >> 4;
+    auto load_q = [&](int k, int r, uint32_t (&f)[4]) {
+        ldmatrix4(q_saddr + r * (16 * D * 2) + ((2 * k + q_hi) ^ q_swz) * 16, f);
+    };
+
+    // addresses within a stage of this lane's rows of the share's first 16 keys, the swizzle folded in: piece c of a
+    // row's block is at the address ^ 16 c; K's rows are blocks of 8 keys in lanes 0-15 and 16-31 (the lanes' bit 3
+    // chooses the piece of a pair), V's in lanes 0-7 and 8-15 (bit 4)
     constexpr int kMask = C::kBlock == 128 ? 7 : 3, kShift = C::kBlock == 128 ? 0 : 1;
+    constexpr int kPieces = C::kBlock / 16;                  // 16-byte pieces of a block
     const uint32_t block_bytes = sub * C::kBlock;            // from one block of a row to the next
-    uint32_t k_off[kSteps], v_off[kSteps];
-    int k_swz, v_swz;
+    uint32_t k_lane, v_lane;
     {
         const int kr = (lane & 7) + ((lane >> 4) & 1) * 8, vr = (lane & 7) + ((lane >> 3) & 1) * 8;
-        k_swz = ((kr >> kShift) & kMask);
-        v_swz = ((vr >> kShift) & kMask);
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int key = split * C::kKeys + i * 16;       // 16 keys lie in one box
-            const uint32_t base = key / sub * sub * C::kRow + key % sub * C::kBlock;
-            k_off[i] = base + kr * C::kBlock;
-            v_off[i] = base + vr * C::kBlock;
-        }
+        const int kx = ((kr >> kShift) & kMask) ^ ((lane >> 3) & 1), vx = ((vr >> kShift) & kMask) ^ (lane >> 4);
+        k_lane = smem_u32(sm.kv[0]) + kr * C::kBlock + kx * 16;
+        v_lane = smem_u32(sm.kv[0]) + vr * C::kBlock + vx * 16 + kTile * C::kRow;
     }
-    constexpr int kPieces = C::kBlock / 16;                  // 16-byte pieces of a block
-    const int k_piece = (lane >> 3) & 1, v_piece = lane >> 4;
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m0 = -CUDART_INF_F, m1 = m0, l0 = 0.0f, l1 = 0.0f;
-    const int c2 = 2 * (lane & 3);
-    // keys of this chunk that the lane's two rows see
-    const int r0 = row0 + mt * 16 + (lane >> 2);
-    const int lim0 = len - a.nq + r0 / G + 1 - k0, lim1 = len - a.nq + (r0 + 8) / G + 1 - k0;
-    const int sees_all = len - a.nq + 1 - k0;                // keys below this are seen by every row
+    auto key_at = [&](int key) {                             // a multiple of 16 within the tile: 16 keys lie in one box
+        return (uint32_t)((key >> ss << ss) * C::kRow + (key & (sub - 1)) * C::kBlock);
+    };
+    const int c2 = 2 * (lane & 3), fr = lane >> 2;
     const float sc = a.scale * kLog2e;
     bool ok = true;
 
-    for (int t = 0; t < ntiles && ok; ++t) {
-        const int st = t % C::kStages;
-        if (warp == 0 && t > 0 && t - 1 + C::kStages < ntiles) {
-            ok = wait(&sm.empty[(t - 1) % C::kStages], ((t - 1) / C::kStages) & 1, &sm.dead, a.err);
+    while (left > 0 && ok) {
+        // ------------------------------------------------------ a head's tiles [tile, tile + cnt)
+        const int cnt = min(left, nt - tile);
+        const int kvh = u / g.row_blocks, row0 = u % g.row_blocks * C::kRows, rows = min(C::kRows, g.rows - row0);
+        // the query rows, 16-byte pieces swizzled by row, a warp per row; for the 8-bit cache as f16 after a power of
+        // two, each 16 elements' pairs in the order 0 2 4 6, 1 3 5 7 (pairs of a quad of bytes go to the halves of k)
+        for (int r = warp; r < C::kRows; r += 8) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+            if (r < rows && lane < D / 16) {
+                const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+                const uint4* src =
+                    reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
+                x = src[2 * lane];
+                y = src[2 * lane + 1];
+            }
+            if constexpr (kE4m3) {
+                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                uint32_t top = 0u;                           // largest exponent of the row (bits 7..14 of an element)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7F80u, (w[i] >> 16) & 0x7F80u));
+                top = __reduce_max_sync(0xFFFFFFFFu, top) >> 7;
+                // 2^(127 - top); a row of zeros, or with an infinity or NaN, stays as it is
+                const int e = top == 255u || top == 0u ? 127 : min(max(254 - (int)top, 1), 254);
+                const float up = __int_as_float(e << 23);
+                if (lane == 0) sm.q_scale[r] = __int_as_float(max(254 - e, 1) << 23);
+                x = make_uint4(bf16x2_to_f16x2(w[0], up), bf16x2_to_f16x2(w[2], up), bf16x2_to_f16x2(w[4], up),
+                               bf16x2_to_f16x2(w[6], up));
+                y = make_uint4(bf16x2_to_f16x2(w[1], up), bf16x2_to_f16x2(w[3], up), bf16x2_to_f16x2(w[5], up),
+                               bf16x2_to_f16x2(w[7], up));
+            }
+            if (lane < D / 16) {
+                uint8_t* dst = sm.q + r * (D * 2);
+                *reinterpret_cast<uint4*>(dst + ((2 * lane) ^ (r & 7)) * 16) = x;
+                *reinterpret_cast<uint4*>(dst + ((2 * lane + 1) ^ (r & 7)) * 16) = y;
+            }
+        }
+        named_barrier(1, kConsumers);
+        uint32_t qf[C::kQRegs ? D / 16 : 1][4];
+        if constexpr (C::kQRegs) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) load_q(k, 0, qf[k]);
+        }
+        // of row tile r, rows lane / 4 (e = 0) and 8 below (e = 1)
+        float o[RT][D / 8][4];
+        float m[RT][2], l[RT][2], qs[RT][2];
+        int lim[RT][2];                                      // keys that the row sees
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = (set * RT + r) * 16 + fr + 8 * e;
+                m[r][e] = -CUDART_INF_F, l[r][e] = 0.0f;
+                qs[r][e] = kE4m3 ? sm.q_scale[row] : 1.0f;
+                lim[r][e] = len - a.nq + (row0 + row) / G + 1;
+            }
+        }
+        const int sees_all = len - a.nq + 1;                 // keys below this are seen by every row
+
+        for (int t = (it ^ wg) & 1; t < cnt; t += 2) {
+            const int st = (it + t) % C::kStages;
+            ok = wait(&sm.full[st], ((it + t) / C::kStages) & 1, &sm.dead, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
-            load_tile(t - 1 + C::kStages);
-        }
-        ok = wait(&sm.full[st], (t / C::kStages) & 1, &sm.dead, a.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        const int key0 = t * kTile + split * C::kKeys;       // the share's first key within the chunk
-        if (key0 < n) {
-            const uint32_t kb = smem_u32(sm.kv[st]), vb = kb + kTile * C::kRow;
-            // ---- scores: two column tiles of 8 keys per 16
-            float s[2 * kSteps][4];
-#pragma unroll
-            for (int i = 0; i < 2 * kSteps; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t qk[4];
-                if (C::kQRegs) {
-                    qk[0] = qf[k % (D / 16)][0], qk[1] = qf[k][1], qk[2] = qf[k][2], qk[3] = qf[k][3];
-                } else {
-                    ldmatrix4(q_saddr + ((2 * k + q_hi) ^ q_swz) * 16, qk);
+            const int share0 = (tile + t) * kTile + split * C::kKeys;   // the share's first key
+            if (share0 + C::kKeys > len) {                   // values past the end may hold NaN, and 0 NaN is NaN
+                for (int i = lane; i < C::kKeys * (C::kRow / 16); i += 32) {
+                    const int key = split * C::kKeys + i / (C::kRow / 16), c = i % (C::kRow / 16);
+                    if ((tile + t) * kTile + key >= len)
+                        *reinterpret_cast<uint4*>(sm.kv[st] + kTile * C::kRow + (key >> ss << ss) * C::kRow +
+                                                  c / kPieces * block_bytes + (key & (sub - 1)) * C::kBlock +
+                                                  c % kPieces * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                if constexpr (!kE4m3) {
-                    const int piece = 2 * k + k_piece;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        uint32_t f[4];
-                        ldmatrix4(kb + k_off[i] + piece / kPieces * block_bytes + ((piece % kPieces) ^ k_swz) * 16, f);
-                        mma_bf16_16816(s[2 * i], qk[0], qk[1], qk[2], qk[3], f[0], f[1]);
-                        mma_bf16_16816(s[2 * i + 1], qk[0], qk[1], qk[2], qk[3], f[2], f[3]);
-                    }
-                } else if ((k & 1) == 0) {
-                    // one load of 16 keys x 32 elements serves two steps
-                    uint32_t q2[4];
-                    if (C::kQRegs) {
-                        q2[0] = qf[(k + 1) % (D / 16)][0], q2[1] = qf[(k + 1) % (D / 16)][1];
-                        q2[2] = qf[(k + 1) % (D / 16)][2], q2[3] = qf[(k + 1) % (D / 16)][3];
-                    } else {
-                        ldmatrix4(q_saddr + ((2 * k + 2 + q_hi) ^ q_swz) * 16, q2);
-                    }
-                    const int piece = k + k_piece;
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        uint32_t f[4];
-                        ldmatrix4(kb + k_off[i] + piece / kPieces * block_bytes + ((piece % kPieces) ^ k_swz) * 16, f);
-                        mma_bf16_16816(s[2 * i], qk[0], qk[1], qk[2], qk[3], e4m3_even(f[0]), e4m3_odd(f[0]));
-                        mma_bf16_16816(s[2 * i], q2[0], q2[1], q2[2], q2[3], e4m3_even(f[1]), e4m3_odd(f[1]));
-                        mma_bf16_16816(s[2 * i + 1], qk[0], qk[1], qk[2], qk[3], e4m3_even(f[2]), e4m3_odd(f[2]));
-                        mma_bf16_16816(s[2 * i + 1], q2[0], q2[1], q2[2], q2[3], e4m3_even(f[3]), e4m3_odd(f[3]));
-                    }
-                }
+                fence_async_shared();                        // before a later load takes their place
+                __syncwarp();
             }
-            float2 vs[2 * kSteps];
+#pragma unroll 1
+            for (int step = 0; step < C::kKeys / 16; ++step) {
+                const int key0 = share0 + 16 * step;
+                if (key0 >= len) break;
+                const uint32_t k_at = k_lane + st * C::kStage + key_at(split * C::kKeys + 16 * step);
+                const uint32_t v_at = v_lane + st * C::kStage + key_at(split * C::kKeys + 16 * step);
+                // ---- scores: two column tiles of 8 keys per 16
+                // (with one row tile each sum in two halves, so that half as many products wait for one another)
+                float s[RT][2][4], s2[RT][2][4];
 #pragma unroll
-            for (int i = 0; i < 2 * kSteps; ++i) {
-                float2 ks = make_float2(sc, sc);
-                if constexpr (kE4m3) {
-                    const float* p = &sm.scale[st][split * C::kKeys + 8 * i + c2];
-                    const float2 u = *reinterpret_cast<const float2*>(p);
-                    vs[i] = *reinterpret_cast<const float2*>(p + kTile);
-                    ks = make_float2(u.x * sc, u.y * sc);
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[r][i][x] = s2[r][i][x] = 0.0f;
+                constexpr int kPer = kE4m3 ? 2 : 1;              // steps of 16 elements that one load of keys serves
+#pragma unroll
+                for (int k = 0; k < D / 16; k += kPer) {
+                    uint32_t q[RT][kPer][4];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int u = 0; u < kPer; ++u) {
+                            if constexpr (C::kQRegs) {
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) q[r][u][x] = qf[k + u][x];
+                            } else {
+                                load_q(k + u, r, q[r][u]);
+                            }
+                        }
+                    const int piece = kE4m3 ? k : 2 * k;         // and the next
+                    {
+                        uint32_t f[4];
+                        ldmatrix4((k_at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16), f);
+                        if constexpr (kE4m3) {
+                            const uint32_t x[8] = {e4m3_lo(f[0]), e4m3_hi(f[0]), e4m3_lo(f[1]), e4m3_hi(f[1]),
+                                                   e4m3_lo(f[2]), e4m3_hi(f[2]), e4m3_lo(f[3]), e4m3_hi(f[3])};
+#pragma unroll
+                            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const uint32_t(&y)[4] = q[r][u % kPer];
+                                    auto& z = RT == 1 && u ? s2 : s;
+                                    mma_f16_16816(z[r][0], y[0], y[1], y[2], y[3], x[2 * u], x[2 * u + 1]);
+                                    mma_f16_16816(z[r][1], y[0], y[1], y[2], y[3], x[4 + 2 * u], x[5 + 2 * u]);
+                                }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const uint32_t(&y)[4] = q[r][0];
+                                auto& z = RT == 1 && (k & 1) ? s2 : s;
+                                mma_bf16_16816(z[r][0], y[0], y[1], y[2], y[3], f[0], f[1]);
+                                mma_bf16_16816(z[r][1], y[0], y[1], y[2], y[3], f[2], f[3]);
+                            }
+                        }
+                    }
                 }
-                s[i][0] *= ks.x, s[i][1] *= ks.y, s[i][2] *= ks.x, s[i][3] *= ks.y;
-            }
-            if (key0 + C::kKeys > sees_all) {                // some row does not see some key
+                // ---- scales, and keys that a row does not see
+                float2 vs[2], lv[2];           // the values' scales and their logarithms
+                const bool masked = key0 + 16 > sees_all;
 #pragma unroll
-                for (int i = 0; i < 2 * kSteps; ++i) {
+                for (int i = 0; i < 2; ++i) {
+                    float2 ks = make_float2(sc, sc);
                     const int key = key0 + 8 * i + c2;
-                    if (key >= lim0) s[i][0] = -CUDART_INF_F;
-                    if (key + 1 >= lim0) s[i][1] = -CUDART_INF_F;
-                    if (key >= lim1) s[i][2] = -CUDART_INF_F;
-                    if (key + 1 >= lim1) s[i][3] = -CUDART_INF_F;
-                    if (kE4m3) {                             // scales past the end may be anything
-                        if (key >= n) vs[i].x = 0.0f;
-                        if (key + 1 >= n) vs[i].y = 0.0f;
-                    }
-                }
-            }
-            // ---- running maximum
-            float t0 = -CUDART_INF_F, t1 = t0;
-#pragma unroll
-            for (int i = 0; i < 2 * kSteps; ++i) {
-                t0 = fmaxf(t0, fmaxf(s[i][0], s[i][1]));
-                t1 = fmaxf(t1, fmaxf(s[i][2], s[i][3]));
-            }
-            t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
-            t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2));
-            t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2));
-            const bool g0 = t0 > m0 + kGrow, g1 = t1 > m1 + kGrow;
-            if (__any_sync(0xFFFFFFFFu, g0 || g1)) {
-                const float f0 = g0 ? ex2(m0 - t0) : 1.0f, f1 = g1 ? ex2(m1 - t1) : 1.0f;
-                if (g0) m0 = t0;
-                if (g1) m1 = t1;
-                l0 *= f0, l1 *= f1;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-            }
-            const float n0 = m0 == -CUDART_INF_F ? 0.0f : m0, n1 = m1 == -CUDART_INF_F ? 0.0f : m1;
-            // ---- probabilities, as the second product's rows
-            uint32_t pa[kSteps][4];
-#pragma unroll
-            for (int i = 0; i < 2 * kSteps; ++i) {
-                float p0 = ex2(s[i][0] - n0), p1 = ex2(s[i][1] - n0), p2 = ex2(s[i][2] - n1), p3 = ex2(s[i][3] - n1);
-                l0 += p0 + p1;
-                l1 += p2 + p3;
-                if (kE4m3) p0 *= vs[i].x, p1 *= vs[i].y, p2 *= vs[i].x, p3 *= vs[i].y;
-                pa[i >> 1][2 * (i & 1)] = pack_bf16x2(p0, p1);
-                pa[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(p2, p3);
-            }
-            // ---- O += P V
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int key = key0 + 16 * i;
-                // 16-bit values past the end are zeroed: they may hold NaN, and 0 NaN is NaN
-                const bool tail = !kE4m3 && key + 16 > n;
-                uint32_t z0 = 0xFFFFFFFFu, z1 = z0;
-                if (tail) {
-                    z0 = (key + c2 < n ? 0xFFFFu : 0u) | (key + c2 + 1 < n ? 0xFFFF0000u : 0u);
-                    z1 = (key + 8 + c2 < n ? 0xFFFFu : 0u) | (key + 9 + c2 < n ? 0xFFFF0000u : 0u);
-                }
-#pragma unroll
-                for (int p = 0; p < C::kRow / 32; ++p) {
-                    const int piece = 2 * p + v_piece;
-                    uint32_t f[4];
-                    ldmatrix4_t(vb + v_off[i] + piece / kPieces * block_bytes + ((piece % kPieces) ^ v_swz) * 16, f);
-                    const uint32_t(&x)[4] = pa[i];
                     if constexpr (kE4m3) {
-                        mma_bf16_16816(o[4 * p], x[0], x[1], x[2], x[3], e4m3_even(f[0]), e4m3_even(f[1]));
-                        mma_bf16_16816(o[4 * p + 1], x[0], x[1], x[2], x[3], e4m3_odd(f[0]), e4m3_odd(f[1]));
-                        mma_bf16_16816(o[4 * p + 2], x[0], x[1], x[2], x[3], e4m3_even(f[2]), e4m3_even(f[3]));
-                        mma_bf16_16816(o[4 * p + 3], x[0], x[1], x[2], x[3], e4m3_odd(f[2]), e4m3_odd(f[3]));
-                    } else {
-                        if (tail) f[0] &= z0, f[1] &= z1, f[2] &= z0, f[3] &= z1;
-                        mma_bf16_16816(o[2 * p], x[0], x[1], x[2], x[3], f[0], f[1]);
-                        mma_bf16_16816(o[2 * p + 1], x[0], x[1], x[2], x[3], f[2], f[3]);
+                        const float* p = &sm.scale[st][split * C::kKeys + 16 * step + 8 * i + c2];
+                        const float2 u = *reinterpret_cast<const float2*>(p);
+                        vs[i] = *reinterpret_cast<const float2*>(p + kTile);
+                        ks = make_float2(u.x * sc, u.y * sc);
+                        if (key >= len) vs[i].x = 0.0f;            // scales past the end may be anything
+                        if (key + 1 >= len) vs[i].y = 0.0f;
+                        lv[i] = make_float2(fmaxf(lg2(vs[i].x), kLeast), fmaxf(lg2(vs[i].y), kLeast));
+                    }
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            s[r][i][x] = (RT == 1 ? s[r][i][x] + s2[r][i][x] : s[r][i][x]) * ((x & 1 ? ks.y : ks.x) * qs[r][x >> 1]);
+                        if (masked) {
+                            if (key >= lim[r][0]) s[r][i][0] = -CUDART_INF_F;
+                            if (key + 1 >= lim[r][0]) s[r][i][1] = -CUDART_INF_F;
+                            if (key >= lim[r][1]) s[r][i][2] = -CUDART_INF_F;
+                            if (key + 1 >= lim[r][1]) s[r][i][3] = -CUDART_INF_F;
+                        }
+                    }
+                }
+                // ---- running maximum
+                float top[RT][2];
+                bool grow = false;
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    float t0 = -CUDART_INF_F, t1 = t0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if constexpr (kE4m3) {
+                            t0 = fmaxf(t0, fmaxf(s[r][i][0] + lv[i].x, s[r][i][1] + lv[i].y));
+                            t1 = fmaxf(t1, fmaxf(s[r][i][2] + lv[i].x, s[r][i][3] + lv[i].y));
+                        } else {
+                            t0 = fmaxf(t0, fmaxf(s[r][i][0], s[r][i][1]));
+                            t1 = fmaxf(t1, fmaxf(s[r][i][2], s[r][i][3]));
+                        }
+                    }
+                    t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
+                    t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
+                    top[r][0] = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2));
+                    top[r][1] = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2));
+                    grow = grow || top[r][0] > m[r][0] + kGrow || top[r][1] > m[r][1] + kGrow;
+                }
+                if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (top[r][e] > m[r][e] + kGrow) {
+                                const float f = ex2(m[r][e] - top[r][e]);
+                                m[r][e] = top[r][e];
+                                l[r][e] *= f;
+#pragma unroll
+                                for (int i = 0; i < D / 8; ++i) o[r][i][2 * e] *= f, o[r][i][2 * e + 1] *= f;
+                            }
+                }
+                // ---- probabilities, as the second product's rows
+                uint32_t pa[RT][4];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float n0 = m[r][0] == -CUDART_INF_F ? 0.0f : m[r][0], n1 = m[r][1] == -CUDART_INF_F ? 0.0f : m[r][1];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float x0 = ex2(s[r][i][0] - n0), x1 = ex2(s[r][i][1] - n0);
+                        float x2 = ex2(s[r][i][2] - n1), x3 = ex2(s[r][i][3] - n1);
+                        l[r][0] += x0 + x1;
+                        l[r][1] += x2 + x3;
+                        if (kE4m3) x0 *= vs[i].x, x1 *= vs[i].y, x2 *= vs[i].x, x3 *= vs[i].y;
+                        pa[r][2 * i] = pack_p<kE4m3>(x0, x1);
+                        pa[r][2 * i + 1] = pack_p<kE4m3>(x2, x3);
+                    }
+                }
+                // ---- O += P V
+                {
+#pragma unroll
+                    for (int p = 0; p < C::kRow / 32; ++p) {
+                        const int piece = 2 * p;
+                        uint32_t f[4];
+                        ldmatrix4_t((v_at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16), f);
+                        if constexpr (kE4m3) {
+                            // the bytes of a key pair: even elements of both keys, then odd ones
+                            const uint32_t e0 = prmt(f[0], 0u, 0x3120), e1 = prmt(f[1], 0u, 0x3120);
+                            const uint32_t e2 = prmt(f[2], 0u, 0x3120), e3 = prmt(f[3], 0u, 0x3120);
+                            const uint32_t v[8] = {e4m3_lo(e0), e4m3_lo(e1), e4m3_hi(e0), e4m3_hi(e1),
+                                                   e4m3_lo(e2), e4m3_lo(e3), e4m3_hi(e2), e4m3_hi(e3)};
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const uint32_t(&x)[4] = pa[r];
+#pragma unroll
+                                for (int u = 0; u < 4; ++u)
+                                    mma_f16_16816(o[r][4 * p + u], x[0], x[1], x[2], x[3], v[2 * u], v[2 * u + 1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                const uint32_t(&x)[4] = pa[r];
+                                mma_bf16_16816(o[r][2 * p], x[0], x[1], x[2], x[3], f[0], f[1]);
+                                mma_bf16_16816(o[r][2 * p + 1], x[0], x[1], x[2], x[3], f[2], f[3]);
+                            }
+                        }
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[st]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[st]);
-    }
-    if (!ok && warp == 0)                                    // leave no copy in flight behind
-        for (int i = 0; i < C::kStages; ++i)
-            for (int ph = 0; ph < 2; ++ph) mbar_wait_bounded(&sm.full[i], ph, nullptr, 1000000ull);
 
-    // ---- the shares of a tile's keys joined: maxima first, then sums and outputs, halving
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
-    const int fr = lane >> 2;
-    if ((lane & 3) == 0) {
-        sm.ml[warp][fr][0] = m0, sm.ml[warp][fr][1] = l0;
-        sm.ml[warp][fr + 8][0] = m1, sm.ml[warp][fr + 8][1] = l1;
-    }
-    __syncthreads();                                         // every tile is consumed: its memory is free
-    float M0 = -CUDART_INF_F, M1 = M0;
+        // ------------------------------------------------------ the shares joined: maxima and sums first
 #pragma unroll
-    for (int i = 0; i < C::kSplits; ++i) {
-        M0 = fmaxf(M0, sm.ml[i * MT + mt][fr][0]);
-        M1 = fmaxf(M1, sm.ml[i * MT + mt][fr + 8][0]);
-    }
-    float L0 = 0.0f, L1 = 0.0f;
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int i = 0; i < C::kSplits; ++i) {
-        const float u0 = sm.ml[i * MT + mt][fr][0], u1 = sm.ml[i * MT + mt][fr + 8][0];
-        if (u0 != -CUDART_INF_F) L0 += sm.ml[i * MT + mt][fr][1] * ex2(u0 - M0);
-        if (u1 != -CUDART_INF_F) L1 += sm.ml[i * MT + mt][fr + 8][1] * ex2(u1 - M1);
-    }
-    const float f0 = m0 == -CUDART_INF_F ? 0.0f : ex2(m0 - M0), f1 = m1 == -CUDART_INF_F ? 0.0f : ex2(m1 - M1);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
-    float4* buf = reinterpret_cast<float4*>(sm.kv[0]);
-#pragma unroll
-    for (int half = C::kSplits / 2; half > 0; half >>= 1) {
-        if (split >= half && split < 2 * half) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                buf[(((split - half) * MT + mt) * (D / 8) + i) * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        }
-        __syncthreads();
-        if (split < half) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const float4 v = buf[((split * MT + mt) * (D / 8) + i) * 32 + lane];
-                o[i][0] += v.x, o[i][1] += v.y, o[i][2] += v.z, o[i][3] += v.w;
-            }
-        }
-        if (half > 1) __syncthreads();
-    }
-    if (split != 0) return;
-
-    // ---- the rows' outputs, or their part of them
-    const bool whole = len <= g.chunk;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int r = mt * 16 + fr + 8 * e;
-        if (r >= rows) continue;
-        const float M = e ? M1 : M0, L = e ? L1 : L0;
-        const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
-        if (whole) {
-            const float inv = L > 0.0f ? 1.0f / L : L;
-            const int64_t at = (int64_t)(b * a.nq + q) * Hq + h;
-            uint16_t* out = a.out + at * D;
-#pragma unroll
-            for (int i = 0; i < D / 8; i += 2) {
-                const float* x = &o[i][2 * e];
-                const float* y = &o[i + 1][2 * e];
-                if constexpr (kE4m3) {   // columns 16 p + 4 c .. + 3: even and odd tiles interleave
-                    *reinterpret_cast<uint2*>(out + 8 * i + 2 * c2) =
-                        make_uint2(pack_bf16x2(x[0] * inv, y[0] * inv), pack_bf16x2(x[1] * inv, y[1] * inv));
-                } else {
-                    *reinterpret_cast<uint32_t*>(out + 8 * i + c2) = pack_bf16x2(x[0] * inv, x[1] * inv);
-                    *reinterpret_cast<uint32_t*>(out + 8 * i + 8 + c2) = pack_bf16x2(y[0] * inv, y[1] * inv);
+            for (int e = 0; e < 2; ++e) {
+                l[r][e] += __shfl_xor_sync(0xFFFFFFFFu, l[r][e], 1);
+                l[r][e] += __shfl_xor_sync(0xFFFFFFFFu, l[r][e], 2);
+                if ((lane & 3) == 0) {
+                    float* p = sm.ml[share][(set * RT + r) * 16 + fr + 8 * e];
+                    p[0] = m[r][e], p[1] = l[r][e];
                 }
             }
-            if (a.lse && (lane & 3) == 0)
-                a.lse[at] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L == 0.0f ? -CUDART_INF_F : L);
-        } else {
-            const int64_t part = ((int64_t)(b * Hk + kvh) * g.chunks + blockIdx.x) * g.rows + row0 + r;
-            float* out = reinterpret_cast<float*>(a.ws) + part * D;
+        ok = named_barrier_and(1, kConsumers, ok);           // all leave if one gave up
 #pragma unroll
-            for (int i = 0; i < D / 8; i += 2) {
-                const float* x = &o[i][2 * e];
-                const float* y = &o[i + 1][2 * e];
-                if constexpr (kE4m3) {
-                    *reinterpret_cast<float4*>(out + 8 * i + 2 * c2) = make_float4(x[0], y[0], x[1], y[1]);
-                } else {
-                    *reinterpret_cast<float2*>(out + 8 * i + c2) = make_float2(x[0], x[1]);
-                    *reinterpret_cast<float2*>(out + 8 * i + 8 + c2) = make_float2(y[0], y[1]);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = (set * RT + r) * 16 + fr + 8 * e;
+                float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+                for (int i = 0; i < C::kShares; ++i) M = fmaxf(M, sm.ml[i][row][0]);
+#pragma unroll
+                for (int i = 0; i < C::kShares; ++i) {
+                    const float x = sm.ml[i][row][0], y = sm.ml[i][row][1];
+                    L += x == -CUDART_INF_F ? y : y * ex2(x - M);   // a share that sees no key holds 0, or a NaN
+                }
+                const float f = m[r][e] == -CUDART_INF_F ? 1.0f : ex2(m[r][e] - M);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) o[r][i][2 * e] *= f, o[r][i][2 * e + 1] *= f;
+                if (share == 0 && (lane & 3) == 0) sm.fin[row][0] = M, sm.fin[row][1] = L;
+            }
+        // outputs: a round each share adds another piece of its columns, so that all work and the order is fixed
+        constexpr int kPairs = D / 16, kPcs = C::kShares < kPairs ? C::kShares : kPairs, kPer2 = kPairs / kPcs;
+#pragma unroll 1
+        for (int round = 0; round < C::kShares; ++round) {
+            const int piece = (share + round) % C::kShares;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                if (i / kPer2 != piece) continue;
+#pragma unroll
+                for (int re = 0; re < 2 * RT; ++re) {
+                    const int r = re >> 1, e = re & 1;
+                    float* dst = sm.acc[(set * RT + r) * 16 + fr + 8 * e] + 16 * i;
+                    const float* x = &o[r][2 * i][2 * e];
+                    const float* y = &o[r][2 * i + 1][2 * e];
+                    if constexpr (kE4m3) {                   // columns 4 c .. + 3: even and odd tiles interleave
+                        float4 v = make_float4(x[0], y[0], x[1], y[1]);
+                        if (round > 0) {
+                            const float4 w = *reinterpret_cast<float4*>(dst + 2 * c2);
+                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                        }
+                        *reinterpret_cast<float4*>(dst + 2 * c2) = v;
+                    } else {
+                        float2 v = make_float2(x[0], x[1]), w = make_float2(y[0], y[1]);
+                        if (round > 0) {
+                            const float2 p = *reinterpret_cast<float2*>(dst + c2), q = *reinterpret_cast<float2*>(dst + 8 + c2);
+                            v.x += p.x, v.y += p.y, w.x += q.x, w.y += q.y;
+                        }
+                        *reinterpret_cast<float2*>(dst + c2) = v;
+                        *reinterpret_cast<float2*>(dst + 8 + c2) = w;
+                    }
                 }
             }
-            if ((lane & 3) == 0) {
-                const int64_t parts = (int64_t)a.B * Hk * g.chunks * g.rows;
-                reinterpret_cast<float2*>(reinterpret_cast<float*>(a.ws) + parts * D)[part] = make_float2(M, L);
+            named_barrier(1, kConsumers);
+        }
+        // ------------------------------------------------------ the rows' outputs, or their part of them
+        const bool whole = cnt == nt;
+        const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);   // a run ends at most one head's start and begins at most one's end
+        for (int i = tid; i < rows * (D / 4); i += kConsumers) {
+            const int r = i / (D / 4), c = i % (D / 4);
+            const float4 v = *reinterpret_cast<const float4*>(&sm.acc[r][4 * c]);
+            const float M = sm.fin[r][0], L = sm.fin[r][1];
+            if (whole) {
+                const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+                const int64_t at = (int64_t)(b * a.nq + q) * Hq + h;
+                const float inv = L > 0.0f ? 1.0f / L : L;
+                *reinterpret_cast<uint2*>(a.out + at * D + 4 * c) =
+                    make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+                if (c == 0 && a.lse) a.lse[at] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L == 0.0f ? -CUDART_INF_F : L);
+            } else {
+                const int64_t at = (int64_t)slot * g.row_pad + r;
+                *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.ws + g.out_at) + at * D + 4 * c) = v;
+                if (c == 0) reinterpret_cast<float2*>(a.ws + g.ml_at)[at] = make_float2(M, L);
             }
         }
+        left -= cnt, it += cnt, tile = 0;
+        if (left > 0 && ++u == U) {
+            u = 0, ++b;
+            len = clamp_len(a.lens[b], a.max_len);
+        }
+        nt = tiles_of(len);
     }
 }
 
-// One query row and head a block: its chunks' outputs, each scaled from its
-// own maximum to the largest, summed and divided.  L lanes hold a row, the
-// other threads take other chunks, so that all loads are in flight at once.
+// 64 columns of one query row and head a block: the outputs that the runs
+// left, each scaled from its own maximum to the largest, summed and divided.
+// 16 lanes hold the columns, 16 groups of them take runs in turn, so that a
+// long row's loads are in flight together.
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_combine(const AttnDecodeArgs a, const DecodeGrid g) {
-    constexpr int L = D / 4, kGroups = 256 / L;
+    constexpr int kGroups = 16;
     __shared__ float red[8], sums[kGroups];
-    __shared__ float4 acc[kGroups][L];
+    __shared__ float4 acc[kGroups][16];
     griddep_launch_dependents();
     griddep_wait();
     const int Hq = a.c.q_heads, Hk = a.c.kv_heads, G = Hq / Hk;
     const int h = blockIdx.x % Hq, q = blockIdx.x / Hq, b = q / a.nq;
-    const int len = min(a.lens[b], a.max_len);
-    if (len <= g.chunk) return;                              // finished by its one chunk
-    const int nc = (len + g.chunk - 1) / g.chunk;
-    const int64_t first = (int64_t)(b * Hk + h / G) * g.chunks * g.rows + (q % a.nq) * G + h % G;
-    const float* po = reinterpret_cast<const float*>(a.ws);
-    const float2* pml = reinterpret_cast<const float2*>(po + (int64_t)a.B * Hk * g.chunks * g.rows * D);
+    const long long* prefix = reinterpret_cast<const long long*>(a.ws);
+    const int row = (q % a.nq) * G + h % G;                  // within the key/value head
+    const int u = h / G * g.row_blocks + row / g.row_pad;
+    const long long all = prefix[a.B] * g.units;
+    const int nt = tiles_of(clamp_len(a.lens[b], a.max_len));
+    const long long s0 = prefix[b] * g.units + (long long)u * nt;
+    const int runs = runs_of(all, g.blocks);
+    // the runs that hold the first and the last tile
+    const int i0 = (int)(((s0 + 1) * runs - 1) / all), i1 = (int)(((s0 + nt) * runs - 1) / all);
+    if (i0 == i1) return;                                    // finished by its one run
+    const int nc = i1 - i0 + 1;
+    const float* po = reinterpret_cast<const float*>(a.ws + g.out_at);
+    const float2* pml = reinterpret_cast<const float2*>(a.ws + g.ml_at);
+    auto part = [&](int c) { return (int64_t)(2 * (i0 + c) + (c == 0 ? 1 : 0)) * g.row_pad + row % g.row_pad; };
     const int tid = threadIdx.x;
     float M = -CUDART_INF_F;
-    for (int c = tid; c < nc; c += 256) M = fmaxf(M, pml[first + (int64_t)c * g.rows].x);
+    for (int c = tid; c < nc; c += 256) M = fmaxf(M, pml[part(c)].x);
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
     if ((tid & 31) == 0) red[tid >> 5] = M;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) M = fmaxf(M, red[i]);
-    const int l = tid % L, grp = tid / L;
+    const int l = tid % 16, grp = tid / 16, col = blockIdx.y * 64 + 4 * l;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
 #pragma unroll 4
     for (int c = grp; c < nc; c += kGroups) {
-        const int64_t part = first + (int64_t)c * g.rows;
-        const float2 ml = pml[part];
-        const float4 v = reinterpret_cast<const float4*>(po + part * D)[l];
-        const float f = ml.x == -CUDART_INF_F ? 0.0f : ex2(ml.x - M);
+        const float2 ml = pml[part(c)];
+        const float4 v = *reinterpret_cast<const float4*>(po + part(c) * D + col);
+        const float f = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - M);   // a run with no key seen: zeros, or NaN
         sum += ml.y * f;
         s.x = fmaf(v.x, f, s.x), s.y = fmaf(v.y, f, s.y), s.z = fmaf(v.z, f, s.z), s.w = fmaf(v.w, f, s.w);
     }
     acc[grp][l] = s;
     if (l == 0) sums[grp] = sum;
     __syncthreads();
+    if (tid >= 16) return;
     float total = 0.0f;
+    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) total += sums[i];
-    const int64_t at = (int64_t)q * Hq + h;
-    if (tid < L) {
-        float4 t = acc[0][tid];
-#pragma unroll
-        for (int i = 1; i < kGroups; ++i) {
-            const float4 v = acc[i][tid];
-            t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-        }
-        const float inv = total > 0.0f ? 1.0f / total : total;
-        reinterpret_cast<uint2*>(a.out + at * D)[tid] =
-            make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
+    for (int i = 0; i < kGroups; ++i) {
+        total += sums[i];
+        const float4 v = acc[i][tid];
+        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
     }
-    if (tid == 0 && a.lse)
+    const int64_t at = (int64_t)q * Hq + h;
+    const float inv = total > 0.0f ? 1.0f / total : total;
+    *reinterpret_cast<uint2*>(a.out + at * D + col) =
+        make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
+    if (tid == 0 && blockIdx.y == 0 && a.lse)
         a.lse[at] = total > 0.0f ? (M + log2f(total)) * kLn2 : (total == 0.0f ? -CUDART_INF_F : total);
 }
 
 DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     DecodeGrid g;
+    g.page_shift = 4;
+    while (1 << g.page_shift < c.page_size) ++g.page_shift;
     g.rows = c.q_heads / c.kv_heads * nq;
-    const int per = 16 * row_tiles(g.rows);
-    g.row_blocks = (g.rows + per - 1) / per;
-    // chunks so that there are about four blocks for each place on the device, at least four tiles each
-    const int64_t base = (int64_t)B * c.kv_heads * g.row_blocks;
-    const int64_t want = std::max<int64_t>(1, 8 * kSms / base);
-    int64_t chunk = (max_len + want - 1) / want;
-    chunk = std::min<int64_t>(kMaxChunk, std::max<int64_t>(256, (chunk + kTile - 1) / kTile * kTile));
-    // whole pages, so that a chunk begins with one
-    if (c.page_size > kTile) chunk = (chunk + c.page_size - 1) / c.page_size * c.page_size;
-    g.chunk = (int)chunk;
-    g.chunks = (int)((max_len + chunk - 1) / chunk);
+    g.row_pad = 16 * row_tiles(g.rows, c.head_dim);
+    g.row_blocks = (g.rows + g.row_pad - 1) / g.row_pad;
+    g.units = c.kv_heads * g.row_blocks;
+    // one block a multiprocessor, no more than the longest lengths give work to
+    const int64_t most = (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile);
+    g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most / kMinTiles));
+    g.out_at = (int64_t)align256((size_t)(B + 1) * sizeof(long long));
+    g.ml_at = g.out_at + (int64_t)2 * g.blocks * g.row_pad * c.head_dim * (int64_t)sizeof(float);
     return g;
 }
 
@@ -579,23 +776,23 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
         return cudaErrorInvalidValue;
     static int done[64] = {0};
     const int smem = (int)sizeof(Smem<D, kE4m3, MT>) + 1024;
-    static_assert((sizeof(Smem<D, kE4m3, MT>) + 1024 + 1024) * C::kBlocks <= 233472, "shared memory per SM");
-    static_assert(C::kSplits / 2 * MT * D * 64 <= C::kStages * C::kStage, "the shares' outputs fit the tiles");
+    static_assert(sizeof(Smem<D, kE4m3, MT>) + 1024 <= 232448 && C::kStages >= 2, "shared memory per block");
     cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, MT>, smem, done);
     if (ce != cudaSuccess) return ce;
-    const dim3 grid(g.chunks, a.c.kv_heads * g.row_blocks, a.B);
-    ce = launch_pdl(k_attn_decode<D, kE4m3, MT>, grid, dim3(C::kThreads), (size_t)smem, st, km, vm, a, g);
-    if (ce != cudaSuccess || g.chunks == 1) return ce;
-    return launch_pdl(k_attn_combine<D>, dim3(a.B * a.nq * a.c.q_heads), dim3(256), 0, st, a, g);
+    ce = launch_pdl(k_attn_decode<D, kE4m3, MT>, dim3(g.blocks), dim3(kThreads), (size_t)smem, st, km, vm, a, g);
+    if (ce != cudaSuccess || g.blocks == 1) return ce;
+    return launch_pdl(k_attn_combine<D>, dim3(a.B * a.nq * a.c.q_heads, D / 64), dim3(256), 0, st, a, g);
 }
 
 template <int D, bool kE4m3>
 cudaError_t decode_rows(const AttnDecodeArgs& a, cudaStream_t st) {
     const DecodeGrid g = decode_grid(a.c, a.B, a.nq, a.max_len);
-    switch (row_tiles(g.rows)) {
-        case 1: return decode_launch<D, kE4m3, 1>(a, g, st);
-        case 2: return decode_launch<D, kE4m3, 2>(a, g, st);
-        default: return decode_launch<D, kE4m3, 4>(a, g, st);
+    switch (g.row_pad) {
+        case 16: return decode_launch<D, kE4m3, 1>(a, g, st);
+        case 32: return decode_launch<D, kE4m3, 2>(a, g, st);
+        default:
+            if constexpr (D == 256) return cudaErrorInvalidValue;
+            else return decode_launch<D, kE4m3, 4>(a, g, st);
     }
 }
 
@@ -608,8 +805,7 @@ cudaError_t decode_dim(const AttnDecodeArgs& a, cudaStream_t st) {
 
 size_t attn_decode_ws_bytes(const attn_config_t& c, int B, int nq, int max_len) {
     const DecodeGrid g = decode_grid(c, B, nq, max_len);
-    // per chunk and row: the output in fp32, its maximum and sum
-    return align256(std::max<size_t>(256, (size_t)B * c.kv_heads * g.chunks * g.rows * (c.head_dim + 2) * sizeof(float)));
+    return align256((size_t)(g.ml_at + (int64_t)2 * g.blocks * g.row_pad * (int64_t)sizeof(float2)));
 }
 
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t st) {

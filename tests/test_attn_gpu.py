@@ -397,6 +397,16 @@ def test_decode_long_and_loose_bounds(e4m3):
     run_decode([500], 1, 16, 2, 128, e4m3, 64, 4, gain=8.0)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_many_sequences(e4m3):
+    """More sequences than a block has threads, short and empty ones among
+    them, and one long one behind them."""
+    g = rng(14)
+    lens = [int(n) for n in torch.randint(0, 90, (450,), generator=g)] + [3000, 0, 1]
+    run_decode(lens, 1, 2, 1, 64, e4m3, 16, 15)
+    run_decode(lens[200:], 3, 16, 2, 128, e4m3, 32, 16)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A bad page reads as zeros (score 0, value 0) and is reported; so is a
     length above max_len (cut) or below zero (none)."""
