@@ -5,13 +5,13 @@
 // they are the rows of m16n8k16 products.  The keys of all sequences and heads
 // are cut into tiles of 64, and one resident block a multiprocessor takes an
 // equal run of the whole list of tiles, whatever the sequences' lengths: a
-// producer warp keeps a ring of TMA page loads (K, V and scales, swizzled)
-// full across the ends of sequences, two groups of four warps take alternate
-// tiles.  Each warp keeps the running maximum m, sum l and output O of its
-// rows over its share of the tiles' keys (no exchange inside the loop); where
-// the run leaves a sequence's head, the shares are joined in shared memory.  A
-// head that one block did whole is finished there; of one cut at a run's end
-// (O, m, l) go to the workspace for k_attn_combine.
+// pair of producer warps keeps a ring of loads (TMA boxes of K and V pages,
+// swizzled; scales) full across the ends of sequences, two groups of four
+// warps take alternate tiles.  Each warp keeps the running maximum m, sum l
+// and output O of its rows over its share of the tiles' keys (no exchange
+// inside the loop); where the run leaves a sequence's head, the shares are
+// joined in shared memory.  A head that one block did whole is finished there;
+// of one cut at a run's end (O, m, l) go to the workspace for k_attn_combine.
 //
 // 8-bit cache: the products run in f16, which holds every e4m3 code exactly;
 // a register of four codes becomes two pairs by two conversions, with no
@@ -40,10 +40,11 @@ namespace {
 
 constexpr int kTile = 64;            // keys of a tile
 constexpr int kSms = 148;
-constexpr int kThreads = 384;        // two groups of consumers, a third of which one warp loads
+constexpr int kThreads = 384;        // two groups of consumers, a third of which two warps load
 constexpr int kConsumers = 256;
 // Registers a thread: all start with 168; the third group gives its own up to the others: 2 * 224 + 56 = 3 * 168.
 constexpr int kRegsConsumer = 224, kRegsProducer = 56;
+constexpr int kProducers = 2;        // loading warps
 constexpr int kMinTiles = 2;         // tiles of a run at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -109,20 +110,6 @@ __device__ __forceinline__ int runs_of(long long total, int blocks) {
     return (int)min((long long)blocks, max(1ll, total / kMinTiles));
 }
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 1000000u)) {
-        if (*reinterpret_cast<volatile int*>(dead)) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
-            set_error(err, MOE_ERR_TIMEOUT);
-            *reinterpret_cast<volatile int*>(dead) = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // Codes 0 and 1 (lo) or 2 and 3 (hi) of w as an f16 pair (exact).
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     uint32_t d;
@@ -164,14 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<Smem<D, kE4m3, MT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, ps = g.page_shift;
-    const int ss = min(ps, 6), sub = 1 << ss, nsub = kTile >> ss;   // rows of a TMA box, boxes of a tile
+    const int ss = min(ps, 6), sub = 1 << ss;        // rows of a TMA box
     long long* prefix = reinterpret_cast<long long*>(a.ws);
 
     if (tid == 0) {
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.full[i], kE4m3 ? 33 : 1);          // the loads' bytes, and each lane's scales
             mbar_init(&sm.empty[i], 4);
         }
         sm.dead = 0;
@@ -253,57 +240,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
-        // ------------------------------------------------------ loads: the lanes of warp 8 take a box of a tile each
-        if (warp == 8) {
-            bool ok = true;
-            auto page_at = [&]() {                           // of this lane's box of the tile; -2: past the end
-                const int key = tile * kTile + (lane << ss);
-                return lane < nsub && key < len ? max(a.page_table[b * a.table_stride + (key >> ps)], -1) : -2;
+        // ------------------------------------------------------ loads: two warps take alternate tiles
+        if (warp < 8 + kProducers) {
+            // lanes 0-15 serve K, 16-31 V: of four keys each, the scales (one 16-byte copy) and, where a page's box
+            // begins, the box
+            const int quad = 4 * (lane & 15);
+            const bool is_v = lane >= 16, boxed = (quad & (sub - 1)) == 0;
+            const CUtensorMap* map = is_v ? &v_map : &k_map;
+            const float* scales = is_v ? a.cache.vs : a.cache.ks;
+            const int32_t* table = a.page_table + b * a.table_stride;
+            const int pad_row = (a.cache.num_pages * Hk) << ps;   // outside the map: reads as zeros
+            int kvh = u / g.row_blocks;
+            auto page_at = [&]() {                           // of this lane's keys; -2: past the end
+                const int key = tile * kTile + quad;
+                return key < len ? max(table[key >> ps], -1) : -2;
             };
-            int page = page_at();
+            auto advance = [&]() {                           // to the next tile of the run
+                ++it, --left;
+                if (++tile < nt || left <= 0) return;
+                tile = 0;
+                if (++u == U) {
+                    u = 0, ++b;
+                    len = clamp_len(a.lens[b], a.max_len);
+                    nt = tiles_of(len);
+                    table += a.table_stride;
+                }
+                kvh = u / g.row_blocks;
+            };
+            if (warp > 8) advance();
+            bool ok = true;
+            int page = left > 0 ? page_at() : -2;
             while (left > 0) {
-                const int st = it % C::kStages, kvh = u / g.row_blocks;
+                const int st = it % C::kStages, use = it / C::kStages;
                 const bool in = page != -2, good = in && page >= 0 && page < a.cache.num_pages;
                 if (in && !good) set_error(a.err, MOE_ERR_BOUNDS);
-                // a bad page reads as zeros, from outside the map
-                const int row = good ? ((page * Hk + kvh) << ps) + ((tile * kTile + (lane << ss)) & ((1 << ps) - 1))
-                                     : (a.cache.num_pages * Hk) << ps;
-                ++it, --left;
-                if (++tile == nt) {
-                    tile = 0;
-                    if (++u == U && left > 0) {
-                        u = 0, ++b;
-                        len = clamp_len(a.lens[b], a.max_len);
-                        nt = tiles_of(len);
-                    }
-                }
+                const int row = good ? ((page * Hk + kvh) << ps) + ((tile * kTile + quad) & ((1 << ps) - 1)) : pad_row;
+                for (int i = 0; i < kProducers; ++i) advance();
                 if (left > 0) page = page_at();              // on its way while this tile waits for its place
-                if (it > C::kStages) {
-                    ok = wait(&sm.empty[st], ((it - 1) / C::kStages - 1) & 1, &sm.dead, a.err);
+                if (use > 0) {
+                    ok = mbar_wait_live(&sm.empty[st], (use - 1) & 1, &sm.dead, a.err);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                 }
-                if (kE4m3 && in && !good)
-                    for (int i = 0; i < sub; ++i)
-                        sm.scale[st][(lane << ss) + i] = sm.scale[st][kTile + (lane << ss) + i] = 0.0f;
-                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, in));
-                const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, good));
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&sm.full[st], boxes * sub * C::kRow * 2 + (kE4m3 ? scaled * sub * 8 : 0));
+                const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, in && boxed));
+                if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], boxes * sub * C::kRow);
                 __syncwarp();
-                if (in) {
-                    uint8_t* dst = sm.kv[st] + (lane << ss) * C::kRow;
-                    tma_load_3d(dst, &k_map, 0, row, 0, &sm.full[st]);
-                    tma_load_3d(dst + kTile * C::kRow, &v_map, 0, row, 0, &sm.full[st]);
-                    if (kE4m3 && good) {
-                        bulk_load(&sm.scale[st][lane << ss], a.cache.ks + row, sub * 4, &sm.full[st]);
-                        bulk_load(&sm.scale[st][kTile + (lane << ss)], a.cache.vs + row, sub * 4, &sm.full[st]);
-                    }
+                if (in && boxed)
+                    tma_load_3d(sm.kv[st] + (is_v ? kTile * C::kRow : 0) + quad * C::kRow, map, 0, row, 0, &sm.full[st]);
+                if constexpr (kE4m3) {                       // a bad page's scales are zeros
+                    cp_async16_zfill(smem_u32(&sm.scale[st][(is_v ? kTile : 0) + quad]), scales + (good ? row : 0), good);
+                    cp_async_arrive(&sm.full[st]);
                 }
             }
-            if (!ok)                                         // leave no copy in flight behind
-                for (int i = max(0, it - 1 - C::kStages); i < it - 1; ++i)
-                    mbar_wait_bounded(&sm.full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+            if constexpr (kE4m3) {
+                cp_async_commit();
+                cp_async_wait<0>();
+            }
+            if (!ok) {                                       // leave no copy in flight behind
+                for (int i = 0; i < C::kStages; ++i)
+                    for (int ph = 0; ph < 2; ++ph) mbar_wait_bounded(&sm.full[i], ph, nullptr, 1000000ull);
+            }
         }
         return;
     }
@@ -402,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         for (int t = (it ^ wg) & 1; t < cnt; t += 2) {
             const int st = (it + t) % C::kStages;
-            ok = wait(&sm.full[st], ((it + t) / C::kStages) & 1, &sm.dead, a.err);
+            ok = mbar_wait_live(&sm.full[st], ((it + t) / C::kStages) & 1, &sm.dead, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             const int share0 = (tile + t) * kTile + split * C::kKeys;   // the share's first key

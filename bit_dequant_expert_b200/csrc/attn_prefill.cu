@@ -129,20 +129,6 @@ __device__ bool find_work(const AttnPrefillArgs& a, int item, int G, int* sh, in
     return seq >= 0;
 }
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* dead, int32_t* err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 1000000u)) {
-        if (*reinterpret_cast<volatile int*>(dead)) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
-            set_error(err, MOE_ERR_TIMEOUT);
-            *reinterpret_cast<volatile int*>(dead) = 1;
-            return false;
-        }
-    }
-    return true;
-}
-
 // O row (D columns from taddr of this thread's lane) times f.
 template <int D>
 __device__ __forceinline__ void rescale_row(uint32_t taddr, float f) {
@@ -256,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool ok = true;
                 auto load = [&](const CUtensorMap* map, int row, int block) {
                     const int i = n % C::kSlots;
-                    if (n >= C::kSlots) ok = ok && wait(&sm.slot_empty[i], (n / C::kSlots - 1) & 1, &sm.dead, a.err);
+                    if (n >= C::kSlots) ok = ok && mbar_wait_live(&sm.slot_empty[i], (n / C::kSlots - 1) & 1, &sm.dead, a.err);
                     if (!ok) return;
                     mbar_arrive_expect_tx(&sm.slot_full[i], C::kSlot);
                     tma_load_3d(sm.slot[i], map, 0, row, block, &sm.slot_full[i]);
@@ -286,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nb > 0) {
                 constexpr uint32_t kIdS = idesc_bf16_f32(kM, kN);
                 constexpr uint32_t kIdO = idesc_bf16_f32_bmn(kM, D);
-                bool ok = wait(&sm.q_full, 0, &sm.dead, a.err);
+                bool ok = mbar_wait_live(&sm.q_full, 0, &sm.dead, a.err);
                 int n = 0;   // slots taken so far
                 // waits for the slots of the next K or V block; returns the first's index
                 auto take = [&]() {
                     const int first = n;
                     for (int p = 0; p < C::kParts; ++p, ++n)
-                        ok = ok && wait(&sm.slot_full[n % C::kSlots], (n / C::kSlots) & 1, &sm.dead, a.err);
+                        ok = ok && mbar_wait_live(&sm.slot_full[n % C::kSlots], (n / C::kSlots) & 1, &sm.dead, a.err);
                     return first;
                 };
                 auto release = [&](int first) {
@@ -360,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool have = false;
                         for (int s = 0; s < 2 && ok; ++s) {
                             if (j < w.nb[s]) {
-                                ok = wait(&sm.p_full[s], j & 1, &sm.dead, a.err);
+                                ok = mbar_wait_live(&sm.p_full[s], j & 1, &sm.dead, a.err);
                                 tc_fence_after();
                                 if (ok) product_o(s, s, vf, j > 0);
                             }
@@ -391,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const int vf = take();
                         if (j == nb - 1 && ok) zero_tail(vf);
-                        ok = ok && wait(&sm.p_full[j & 1], (j >> 1) & 1, &sm.dead, a.err);
+                        ok = ok && mbar_wait_live(&sm.p_full[j & 1], (j >> 1) & 1, &sm.dead, a.err);
                         tc_fence_after();
                         if (ok) {
                             product_o(0, j & 1, vf, j > 0);
@@ -422,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = C::kStreams == 2 ? 0 : grp; j < blocks && ok; j += C::kStreams == 2 ? 1 : 2) {
             const int buf = C::kStreams == 2 ? s : (j & 1);
             const uint32_t phase = C::kStreams == 2 ? (j & 1) : ((j >> 1) & 1);
-            ok = wait(&sm.s_full[buf], phase, &sm.dead, a.err);
+            ok = mbar_wait_live(&sm.s_full[buf], phase, &sm.dead, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -450,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
             if (C::kStreams == 1 && j > 0) {   // the maximum as the other group left it
-                ok = wait(&sm.m_full[buf ^ 1], ((j - 1) >> 1) & 1, &sm.dead, a.err);
+                ok = mbar_wait_live(&sm.m_full[buf ^ 1], ((j - 1) >> 1) & 1, &sm.dead, a.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 m = sm.m[buf ^ 1][r];
@@ -471,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l *= f;
             }
             if (j > 0 && __any_sync(0xFFFFFFFFu, grow)) {
-                ok = wait(&sm.o_done[s], (j - 1) & 1, &sm.dead, a.err);
+                ok = mbar_wait_live(&sm.o_done[s], (j - 1) & 1, &sm.dead, a.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -510,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // both groups end on the last maximum and the sum of both sums, and store half of the columns each
             if (blocks > 0) {
                 if (((blocks - 1) & 1) != grp && ok)
-                    ok = wait(&sm.m_full[(blocks - 1) & 1], ((blocks - 1) >> 1) & 1, &sm.dead, a.err);
+                    ok = mbar_wait_live(&sm.m_full[(blocks - 1) & 1], ((blocks - 1) >> 1) & 1, &sm.dead, a.err);
                 m = sm.m[(blocks - 1) & 1][r];
             }
             if (m != m_own) l *= ex2(m_own - m);
@@ -524,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = w.live[s] && row < w.lq;
         const int64_t at = (int64_t)(w.q0 + row) * a.c.q_heads + w.head[s];
         if (blocks > 0 && ok) {
-            ok = wait(&sm.o_done[s], (blocks - 1) & 1, &sm.dead, a.err);
+            ok = mbar_wait_live(&sm.o_done[s], (blocks - 1) & 1, &sm.dead, a.err);
             tc_fence_after();
             const float inv = l > 0.0f ? 1.0f / l : l;   // l = 0: no key; NaN stays
             store_row(o_addr, c0, c1, inv, a.out + at * D, valid && ok);

@@ -79,6 +79,23 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
     return true;
 }
 
+// The same among the roles of one block: *dead (shared memory) is set when a
+// wait expires, and ends the others' waits.  Time is counted in SM clocks: 4e9
+// are 2 to 4 seconds.
+__device__ __forceinline__ bool mbar_wait_live(uint64_t* bar, uint32_t parity, int* dead, int32_t* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*reinterpret_cast<volatile int*>(dead)) return false;
+        if (clock64() - t0 > 4000000000ll) {
+            if (err) atomicCAS(err, 0, 6 /* MOE_ERR_TIMEOUT */);
+            *reinterpret_cast<volatile int*>(dead) = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // ------------------------------------------------------------------ copies
 
 // ------------------------------------------------------------------ cross-CTA words
@@ -414,6 +431,15 @@ __device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, 
 // 4-byte async copy global -> shared (both 4-byte aligned).
 __device__ __forceinline__ void cp_async4(uint32_t dst_saddr, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_saddr), "l"(src) : "memory");
+}
+// 16-byte async copy global -> shared, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst_saddr, const void* src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_saddr), "l"(src), "r"(copy ? 16 : 0)
+                 : "memory");
+}
+// Arrives once on `bar` (an arrival it counts on) when this thread's cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
