@@ -96,8 +96,14 @@ struct DecodeGrid {
     int rows, row_blocks;            // query rows of a key/value head, passes of 16 MT of them
     int units;                       // heads x passes of a sequence
     int row_pad;                     // 16 MT
-    int64_t out_at;                  // workspace: tiles before each sequence (int64 [B + 1]), then partial outputs,
-    int64_t ml_at;                   // then their maxima and sums (byte offsets)
+    int64_t out_at;                  // workspace: a Cut a run, then partial outputs, then their maxima and sums
+    int64_t ml_at;                   // (byte offsets)
+};
+
+// A unit that runs share: left by the second of them (first < 0 in the others' places).
+struct Cut {
+    int first, count;                // the run that holds its first tile, and how many hold some
+    int b, u;                        // sequence, head and pass
 };
 
 // Tiles of a sequence's unit; an empty one has a tile without keys, which writes its zeros.
@@ -152,7 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, ps = g.page_shift;
     const int ss = min(ps, 6), sub = 1 << ss;        // rows of a TMA box
-    long long* prefix = reinterpret_cast<long long*>(a.ws);
 
     if (tid == 0) {
         prefetch_tensormap(&k_map);
@@ -191,15 +196,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w < warp) before += sm.scan[w];
             total += sm.scan[w];
         }
-        if (b < a.B && blockIdx.x == 0) prefix[b] = before;
         if (base == 0) first_before = before, first_n = n;
         __syncthreads();
     }
-    if (tid == 0 && blockIdx.x == 0) prefix[a.B] = total;
     const int U = g.units;
     total *= U;
     const int runs = runs_of(total, gridDim.x);
-    if ((int)blockIdx.x >= runs) return;
+    Cut* cuts = reinterpret_cast<Cut*>(a.ws);
+    if ((int)blockIdx.x >= runs) {
+        if (tid == 0) cuts[blockIdx.x].first = -1;
+        return;
+    }
     const long long start = run_start(total, blockIdx.x, runs), end = run_start(total, blockIdx.x + 1, runs);
     {
         const long long at = start / U;
@@ -237,6 +244,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long rem = start - sm.scan[12] * U;
     int u = (int)(rem / nt), tile = (int)(rem % nt);
     int left = (int)(end - start), it = 0;                   // tiles of the run to go, and done
+    if (tid == 0) {
+        Cut c = {-1, 0, b, u};
+        if (tile > 0) {                                      // the runs that hold the unit's first and last tile
+            const long long s0 = start - tile;
+            c.first = (int)(((s0 + 1) * runs - 1) / total);
+            c.count = (int)(((s0 + nt) * runs - 1) / total) - c.first + 1;
+            if (c.first != (int)blockIdx.x - 1) c.first = -1;
+        }
+        cuts[blockIdx.x] = c;
+    }
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
@@ -679,70 +696,105 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// 64 columns of one query row and head a block: the outputs that the runs
-// left, each scaled from its own maximum to the largest, summed and divided.
-// 16 lanes hold the columns, 16 groups of them take runs in turn, so that a
-// long row's loads are in flight together.
+// Joins the outputs that the runs left of a unit (block x: the one whose
+// second run is x + 1), each scaled from its own maximum to the largest,
+// summed and divided.  A warp holds a row; of two to four runs it takes all,
+// of more the block's eight warps take runs in turn, so that a long row's
+// loads are in flight together, and are joined in shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) k_attn_combine(const AttnDecodeArgs a, const DecodeGrid g) {
-    constexpr int kGroups = 16;
-    __shared__ float red[8], sums[kGroups];
-    __shared__ float4 acc[kGroups][16];
+    constexpr int kV = D >= 128 ? 4 : 2, kN = D / 32 / kV;   // a lane's columns: kN vectors of kV
+    __shared__ float acc[8][D];
+    __shared__ float2 ms[8];
     griddep_launch_dependents();
     griddep_wait();
+    const Cut c = reinterpret_cast<const Cut*>(a.ws)[blockIdx.x + 1];
+    if (c.first < 0) return;
     const int Hq = a.c.q_heads, Hk = a.c.kv_heads, G = Hq / Hk;
-    const int h = blockIdx.x % Hq, q = blockIdx.x / Hq, b = q / a.nq;
-    const long long* prefix = reinterpret_cast<const long long*>(a.ws);
-    const int row = (q % a.nq) * G + h % G;                  // within the key/value head
-    const int u = h / G * g.row_blocks + row / g.row_pad;
-    const long long all = prefix[a.B] * g.units;
-    const int nt = tiles_of(clamp_len(a.lens[b], a.max_len));
-    const long long s0 = prefix[b] * g.units + (long long)u * nt;
-    const int runs = runs_of(all, g.blocks);
-    // the runs that hold the first and the last tile
-    const int i0 = (int)(((s0 + 1) * runs - 1) / all), i1 = (int)(((s0 + nt) * runs - 1) / all);
-    if (i0 == i1) return;                                    // finished by its one run
-    const int nc = i1 - i0 + 1;
+    const int kvh = c.u / g.row_blocks, row0 = c.u % g.row_blocks * g.row_pad, rows = min(g.row_pad, g.rows - row0);
     const float* po = reinterpret_cast<const float*>(a.ws + g.out_at);
     const float2* pml = reinterpret_cast<const float2*>(a.ws + g.ml_at);
-    auto part = [&](int c) { return (int64_t)(2 * (i0 + c) + (c == 0 ? 1 : 0)) * g.row_pad + row % g.row_pad; };
-    const int tid = threadIdx.x;
-    float M = -CUDART_INF_F;
-    for (int c = tid; c < nc; c += 256) M = fmaxf(M, pml[part(c)].x);
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    if ((tid & 31) == 0) red[tid >> 5] = M;
-    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool split = c.count > 4;
+    for (int base = blockIdx.y * (split ? 1 : 8); base < rows; base += gridDim.y * (split ? 1 : 8)) {
+        const int r = split ? base : base + warp;
+        float M = -CUDART_INF_F, L = 0.0f, o[kN][kV];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) M = fmaxf(M, red[i]);
-    const int l = tid % 16, grp = tid / 16, col = blockIdx.y * 64 + 4 * l;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < kV; ++e) o[n][e] = 0.0f;
+        if (r < rows) {
 #pragma unroll 4
-    for (int c = grp; c < nc; c += kGroups) {
-        const float2 ml = pml[part(c)];
-        const float4 v = *reinterpret_cast<const float4*>(po + part(c) * D + col);
-        const float f = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - M);   // a run with no key seen: zeros, or NaN
-        sum += ml.y * f;
-        s.x = fmaf(v.x, f, s.x), s.y = fmaf(v.y, f, s.y), s.z = fmaf(v.z, f, s.z), s.w = fmaf(v.w, f, s.w);
-    }
-    acc[grp][l] = s;
-    if (l == 0) sums[grp] = sum;
-    __syncthreads();
-    if (tid >= 16) return;
-    float total = 0.0f;
-    float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = split ? warp : 0; i < c.count; i += split ? 8 : 1) {
+                // the first run left the unit's head, the others what they began with
+                const int64_t at = (int64_t)(2 * (c.first + i) + (i == 0 ? 1 : 0)) * g.row_pad + r;
+                const float2 ml = pml[at];
+                float x[kN][kV];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-        total += sums[i];
-        const float4 v = acc[i][tid];
-        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+                for (int n = 0; n < kN; ++n) {
+                    const float* src = po + at * D + (n * 32 + lane) * kV;
+                    if constexpr (kV == 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(src);
+                        x[n][0] = v.x, x[n][1] = v.y, x[n][2] = v.z, x[n][3] = v.w;
+                    } else {
+                        const float2 v = *reinterpret_cast<const float2*>(src);
+                        x[n][0] = v.x, x[n][1] = v.y;
+                    }
+                }
+                const float m = fmaxf(M, ml.x);
+                // a run with no key seen holds zeros, or NaN
+                const float f = M == -CUDART_INF_F ? 1.0f : ex2(M - m), h = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - m);
+                M = m;
+                L = L * f + ml.y * h;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) o[n][e] = o[n][e] * f + x[n][e] * h;
+            }
+        }
+        if (split) {
+            if (lane == 0) ms[warp] = make_float2(M, L);
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[warp][(n * 32 + lane) * kV + e] = o[n][e];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) M = fmaxf(M, ms[i].x);
+                L = 0.0f;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) o[n][e] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float h = ms[i].x == -CUDART_INF_F ? 1.0f : ex2(ms[i].x - M);
+                    L += ms[i].y * h;
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int e = 0; e < kV; ++e) o[n][e] += acc[i][(n * 32 + lane) * kV + e] * h;
+                }
+            }
+            __syncthreads();
+        }
+        if (r < rows && (!split || warp == 0)) {
+            const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+            const int64_t at = (int64_t)(c.b * a.nq + q) * Hq + h;
+            const float inv = L > 0.0f ? 1.0f / L : L;
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                uint16_t* dst = a.out + at * D + (n * 32 + lane) * kV;
+                if constexpr (kV == 4)
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[n][0] * inv, o[n][1] * inv),
+                                                                pack_bf16x2(o[n][2] * inv, o[n][3] * inv));
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[n][0] * inv, o[n][1] * inv);
+            }
+            if (lane == 0 && a.lse) a.lse[at] = L > 0.0f ? (M + log2f(L)) * kLn2 : (L == 0.0f ? -CUDART_INF_F : L);
+        }
     }
-    const int64_t at = (int64_t)q * Hq + h;
-    const float inv = total > 0.0f ? 1.0f / total : total;
-    *reinterpret_cast<uint2*>(a.out + at * D + col) =
-        make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
-    if (tid == 0 && blockIdx.y == 0 && a.lse)
-        a.lse[at] = total > 0.0f ? (M + log2f(total)) * kLn2 : (total == 0.0f ? -CUDART_INF_F : total);
 }
 
 DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
@@ -756,7 +808,7 @@ DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     // one block a multiprocessor, no more than the longest lengths give work to
     const int64_t most = (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile);
     g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most / kMinTiles));
-    g.out_at = (int64_t)align256((size_t)(B + 1) * sizeof(long long));
+    g.out_at = (int64_t)align256((size_t)g.blocks * sizeof(Cut));
     g.ml_at = g.out_at + (int64_t)2 * g.blocks * g.row_pad * c.head_dim * (int64_t)sizeof(float);
     return g;
 }
@@ -777,7 +829,7 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
     if (ce != cudaSuccess) return ce;
     ce = launch_pdl(k_attn_decode<D, kE4m3, MT>, dim3(g.blocks), dim3(kThreads), (size_t)smem, st, km, vm, a, g);
     if (ce != cudaSuccess || g.blocks == 1) return ce;
-    return launch_pdl(k_attn_combine<D>, dim3(a.B * a.nq * a.c.q_heads, D / 64), dim3(256), 0, st, a, g);
+    return launch_pdl(k_attn_combine<D>, dim3(g.blocks - 1, 4), dim3(256), 0, st, a, g);
 }
 
 template <int D, bool kE4m3>
