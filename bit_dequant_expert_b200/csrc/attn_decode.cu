@@ -1,23 +1,28 @@
 // Attention of a few new tokens per sequence over the paged cache: bound by
 // the bytes of the cache, each read once.
 //
-// The nq G query rows (nq tokens, G heads) of a key/value head share its keys:
-// they are the rows of m16n8k16 products.  The keys of all sequences and heads
-// are cut into tiles of 64, and one resident block a multiprocessor takes an
-// equal run of the whole list of tiles, whatever the sequences' lengths: a
-// pair of producer warps keeps a ring of loads (TMA boxes of K and V pages,
-// swizzled; scales) full across the ends of sequences, two groups of four
-// warps take alternate tiles.  Each warp keeps the running maximum m, sum l
-// and output O of its rows over its share of the tiles' keys (no exchange
-// inside the loop); where the run leaves a sequence's head, the shares are
-// joined in shared memory.  A head that one block did whole is finished there;
-// of one cut at a run's end (O, m, l) go to the workspace for k_attn_combine.
+// The nq G query rows (nq tokens, G heads) of a key/value head share its keys.
+// The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that a
+// m16n8k16 has 16 keys (or elements of V) by 8 query rows: eight heads fill
+// it.  The keys of all sequences and heads are cut into tiles of 64, and one
+// resident block a multiprocessor takes an equal run of the whole list of
+// tiles, whatever the sequences' lengths.  Two producer warps keep a ring of
+// loads (TMA boxes of K and V pages, swizzled; scales) full across the ends of
+// sequences, two more bring the next head's queries.  Groups of four warps
+// take tiles in turn: a warp forms the scores of 16 keys against all rows, the
+// probabilities go to its group through shared memory, and it adds all 64
+// keys' values to a quarter of the output's columns, so that outputs take few
+// registers and no key is converted twice.  A group keeps the running maximum
+// m of each row, exchanged only when some score exceeds it by 2^8.  Where the
+// run leaves a sequence's head, the groups are joined in shared memory.  A
+// head that one block did whole is finished there; of one cut at a run's end
+// (O, m, l) go to the workspace for k_attn_combine.
 //
 // 8-bit cache: the products run in f16, which holds every e4m3 code exactly;
 // a register of four codes becomes two pairs by two conversions, with no
 // shuffles: the queries are laid out for the order in which the bytes come,
-// and a transposed load of byte pairs gives the even and the odd elements of
-// V as two column tiles.  A query row is brought to a largest magnitude in
+// and a transposed load of byte pairs gives the even elements of V as a tile's
+// rows 0-7, the odd ones as 8-15.  A query row is brought to a largest magnitude in
 // [1, 2) by a power of two (exact: bf16 has fewer bits; what falls below
 // 2^-24 of the row's largest is under the sums' own rounding), a key's scale
 // multiplies its score, a value's its probability.  The running maximum m is
@@ -40,10 +45,6 @@ namespace {
 
 constexpr int kTile = 64;            // keys of a tile
 constexpr int kSms = 148;
-constexpr int kThreads = 384;        // two groups of consumers, a third of which two warps load
-constexpr int kConsumers = 256;
-// Registers a thread: all start with 168; the third group gives its own up to the others: 2 * 224 + 56 = 3 * 168.
-constexpr int kRegsConsumer = 224, kRegsProducer = 56;
 constexpr int kProducers = 2;        // loading warps
 constexpr int kMinTiles = 2;         // tiles of a run at least
 constexpr float kLog2e = 1.4426950408889634f;
@@ -51,41 +52,42 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -100.0f;    // log2 of the least value scale the running maximum follows
 constexpr float kGrow = 8.0f;        // log2 of the growth of a row's maximum that O is rescaled for
 
-// Tiles of 16 query rows that a block works on at once (more rows take more passes over the keys).
-int row_tiles(int rows, int dim) { return rows <= 16 ? 1 : rows <= 32 || dim == 256 ? 2 : 4; }
+// Tiles of 8 query rows that a block works on at once (more rows take more passes over the keys).
+int row_tiles(int rows, int dim) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 || dim == 256 ? 4 : 8; }
 
-template <int D, bool kE4m3, int MT>
+template <int D, bool kE4m3, int NT>
 struct Cfg {
-    // Row tiles of one warp: two where its outputs fit the registers, so that a key's fragments (and their
-    // conversions) serve 32 rows; the sets of warps of a group that share out the row tiles
-    static constexpr int kRT = MT == 1 || D == 256 ? 1 : 2;
-    static constexpr int kSets = MT / kRT;
-    static constexpr int kSplits = 4 / kSets;                // shares of a tile's keys
-    static constexpr int kKeys = kTile / kSplits;            // keys of a share: 16 or 32
-    static constexpr int kShares = 2 * kSplits;              // of a row tile, both groups
+    // groups of four warps that take tiles in turn: three where 128 registers a thread hold a warp's work, else two
+    static constexpr int kGroups = D * NT <= 256 ? 3 : 2;
+    static constexpr int kConsumers = 128 * kGroups;
+    static constexpr int kThreads = kConsumers + 128;
+    static constexpr int kCols = D / 64;                     // tiles of 16 columns of the output a warp has
     static constexpr int kRow = D * (kE4m3 ? 1 : 2);         // bytes of a cache row
     static constexpr int kBlock = kRow < 128 ? kRow : 128;   // swizzled bytes of a row's blocks
     static constexpr int kStage = 2 * kTile * kRow;          // K and V of a tile
-    static constexpr int kPad = kE4m3 ? 16 : 8;              // floats between output rows: no bank conflicts
-    static constexpr int kRows = 16 * MT;
-    static constexpr int kRest = kRows * (D * 2 + (D + kPad) * 4 + kShares * 8 + 16) + 1024;
+    static constexpr int kPad = 4;                           // floats between output rows: no bank conflicts
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRest =
+        kRows * (D * 4 + (D + kPad) * 4 + 8 * 4 * kGroups + 4 * kGroups + 16) + kGroups * NT * 1024 + 1024;
     static constexpr int kFit = (226 * 1024 - kRest) / (kStage + kTile * 8 + 16);
     static constexpr int kStages = kFit > 12 ? 12 : kFit;
-    static constexpr bool kQRegs = D <= 128 && kRT == 1;     // query fragments in registers
+    static constexpr bool kQRegs = NT == 1 && D <= 128;       // query fragments in registers
 };
 
-template <int D, bool kE4m3, int MT>
+template <int D, bool kE4m3, int NT>
 struct Smem {
-    using C = Cfg<D, kE4m3, MT>;
+    using C = Cfg<D, kE4m3, NT>;
     uint8_t kv[C::kStages][C::kStage];                       // 1024-aligned
-    uint8_t q[C::kRows * D * 2];
+    uint8_t q[2][C::kRows * D * 2];                          // this head's and the next one's
+    uint2 p[C::kGroups][4][NT][32];                          // probabilities of 16 keys, as the second product reads them
     float acc[C::kRows][D + C::kPad];
     float scale[C::kStages][kE4m3 ? 2 * kTile : 4];          // K's, then V's
-    uint64_t full[C::kStages], empty[C::kStages];
-    float ml[C::kShares][C::kRows][2];
+    uint64_t full[C::kStages], empty[C::kStages], q_full[2], q_empty[2];
+    float top[C::kGroups][4][C::kRows];                      // a group's maxima of a tile
+    float m[C::kGroups][C::kRows], l[C::kGroups][4][C::kRows];
     float fin[C::kRows][2];
-    float q_scale[C::kRows];
-    long long scan[14];
+    float q_scale[2][C::kRows];
+    long long scan[20];                                      // warps' sums, then the run's first sequence
     int find;
     int dead;
 };
@@ -93,9 +95,9 @@ struct Smem {
 struct DecodeGrid {
     int blocks;                      // blocks launched
     int page_shift;                  // log2 of page_size
-    int rows, row_blocks;            // query rows of a key/value head, passes of 16 MT of them
+    int rows, row_blocks;            // query rows of a key/value head, passes of row_pad of them
     int units;                       // heads x passes of a sequence
-    int row_pad;                     // 16 MT
+    int row_pad;                     // 8 NT
     int64_t out_at;                  // workspace: a Cut a run, then partial outputs, then their maxima and sums
     int64_t ml_at;                   // (byte offsets)
 };
@@ -141,20 +143,34 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) { retur
 template <bool kE4m3>
 __device__ __forceinline__ uint32_t pack_p(float lo, float hi) { return kE4m3 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi); }
 
+template <bool kF16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (kF16) mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    else mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+// 16 elements by 16 keys of V from a transposed load of byte pairs of keys 0-7 and 8-15: the bytes of a key pair are
+// put in order, even elements of both keys, then odd ones (rows 0-7 and 8-15 of the product).
+__device__ __forceinline__ void v_rows(uint32_t lo, uint32_t hi, uint32_t (&f)[4]) {
+    const uint32_t x = prmt(lo, 0u, 0x3120), y = prmt(hi, 0u, 0x3120);
+    f[0] = e4m3_lo(x), f[1] = e4m3_hi(x), f[2] = e4m3_lo(y), f[3] = e4m3_hi(y);
+}
+
 __device__ __forceinline__ float lg2(float x) {
     float r;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 
-template <int D, bool kE4m3, int MT>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kE4m3, int NT>
+__global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     k_attn_decode(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const AttnDecodeArgs a, const DecodeGrid g) {
-    using C = Cfg<D, kE4m3, MT>;
+    using C = Cfg<D, kE4m3, NT>;
+    constexpr int kThreads = C::kThreads, kConsumers = C::kConsumers;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem<D, kE4m3, MT>& sm =
-        *reinterpret_cast<Smem<D, kE4m3, MT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<D, kE4m3, NT>& sm =
+        *reinterpret_cast<Smem<D, kE4m3, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, ps = g.page_shift;
     const int ss = min(ps, 6), sub = 1 << ss;        // rows of a TMA box
@@ -165,6 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sm.full[i], kE4m3 ? 33 : 1);          // the loads' bytes, and each lane's scales
             mbar_init(&sm.empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 64);
+            mbar_init(&sm.q_empty[i], 1);
         }
         sm.dead = 0;
         fence_mbar_init();
@@ -212,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at = start / U;
         if (tid < a.B && at >= first_before && at < first_before + first_n) {
             sm.find = tid;
-            sm.scan[12] = first_before;
+            sm.scan[16] = first_before;
         }
         // more sequences than threads: later ones by another pass over their lengths
         long long before0 = 0;
@@ -235,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncthreads();
             if (n > 0 && at >= before && at < before + n) {
                 sm.find = b;
-                sm.scan[12] = before;
+                sm.scan[16] = before;
             }
         }
         __syncthreads();
     }
     int b = sm.find, len = clamp_len(a.lens[b], a.max_len), nt = tiles_of(len);
-    const long long rem = start - sm.scan[12] * U;
+    const long long rem = start - sm.scan[16] * U;
     int u = (int)(rem / nt), tile = (int)(rem % nt);
     int left = (int)(end - start), it = 0;                   // tiles of the run to go, and done
     if (tid == 0) {
@@ -255,10 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         cuts[blockIdx.x] = c;
     }
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+    if (tid >= kConsumers) {
+        const int pw = warp - kConsumers / 32;
         // ------------------------------------------------------ loads: two warps take alternate tiles
-        if (warp < 8 + kProducers) {
+        if (pw < kProducers) {
             // lanes 0-15 serve K, 16-31 V: of four keys each, the scales (one 16-byte copy) and, where a page's box
             // begins, the box
             const int quad = 4 * (lane & 15);
@@ -284,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 kvh = u / g.row_blocks;
             };
-            if (warp > 8) advance();
+            for (int i = 0; i < pw; ++i) advance();
             bool ok = true;
             int page = left > 0 ? page_at() : -2;
             while (left > 0) {
@@ -317,284 +337,303 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < C::kStages; ++i)
                     for (int ph = 0; ph < 2; ++ph) mbar_wait_bounded(&sm.full[i], ph, nullptr, 1000000ull);
             }
+        } else {
+            // -------------------------------------------------- queries of the run's heads, one ahead
+            for (int n = 0; left > 0; ++n) {
+                const int buf = n & 1;
+                const int kvh = u / g.row_blocks, row0 = u % g.row_blocks * C::kRows, rows = min(C::kRows, g.rows - row0);
+                if (n > 1) {
+                    bool ok = mbar_wait_live(&sm.q_empty[buf], (n / 2 - 1) & 1, &sm.dead, a.err);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                }
+                // the query rows, 16-byte pieces swizzled by row, D / 16 lanes a row; for the 8-bit cache as f16 after a
+                // power of two, each 16 elements' pairs in the order 0 2 4 6, 1 3 5 7 (pairs of a quad of bytes go to
+                // the halves of k)
+                constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes;
+                const int c = lane % kLanes;
+#pragma unroll 2
+                for (int r0 = (pw - kProducers) * kAtOnce; r0 < C::kRows; r0 += (4 - kProducers) * kAtOnce) {
+                    const int r = r0 + lane / kLanes;
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+                    if (r < rows) {
+                        const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+                        const uint4* src =
+                            reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
+                        x = src[2 * c];
+                        y = src[2 * c + 1];
+                    }
+                    if constexpr (kE4m3) {
+                        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                        uint32_t top = 0u;                   // largest exponent of the row (bits 7..14 of an element)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7F80u, (w[i] >> 16) & 0x7F80u));
+#pragma unroll
+                        for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        top >>= 7;
+                        // 2^(127 - top); a row of zeros, or with an infinity or NaN, stays as it is
+                        const int e = top == 255u || top == 0u ? 127 : min(max(254 - (int)top, 1), 254);
+                        const float up = __int_as_float(e << 23);
+                        if (c == 0 && r < C::kRows) sm.q_scale[buf][r] = __int_as_float(max(254 - e, 1) << 23);
+                        x = make_uint4(bf16x2_to_f16x2(w[0], up), bf16x2_to_f16x2(w[2], up), bf16x2_to_f16x2(w[4], up),
+                                       bf16x2_to_f16x2(w[6], up));
+                        y = make_uint4(bf16x2_to_f16x2(w[1], up), bf16x2_to_f16x2(w[3], up), bf16x2_to_f16x2(w[5], up),
+                                       bf16x2_to_f16x2(w[7], up));
+                    }
+                    if (r < C::kRows) {
+                        uint8_t* dst = sm.q[buf] + r * (D * 2);
+                        *reinterpret_cast<uint4*>(dst + ((2 * c) ^ (r & 7)) * 16) = x;
+                        *reinterpret_cast<uint4*>(dst + ((2 * c + 1) ^ (r & 7)) * 16) = y;
+                    }
+                }
+                mbar_arrive(&sm.q_full[buf]);
+                left -= nt - tile, tile = 0;
+                if (left > 0 && ++u == U) {
+                    u = 0, ++b;
+                    len = clamp_len(a.lens[b], a.max_len);
+                    nt = tiles_of(len);
+                }
+            }
         }
         return;
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
     // ---------------------------------------------------------- products
-    constexpr int RT = C::kRT;
-    const int wg = warp >> 2, set = (warp & 3) % C::kSets, split = (warp & 3) / C::kSets;
-    const int share = wg * C::kSplits + split;
+    const int grp = warp >> 2, w = warp & 3;                 // the group; the warp's 16 keys and quarter of columns
 
-    // fragments of the warp's query rows
-    const uint32_t q_saddr = smem_u32(sm.q) + (set * RT * 16 + (lane & 15)) * (D * 2);
-    const int q_swz = lane & 7, q_hi = lane >> 4;
-    auto load_q = [&](int k, int r, uint32_t (&f)[4]) {
-        ldmatrix4(q_saddr + r * (16 * D * 2) + ((2 * k + q_hi) ^ q_swz) * 16, f);
+    // fragments of the query rows: two steps of 16 elements of a row tile
+    const uint32_t q_lane = smem_u32(sm.q[0]) + (lane & 7) * (D * 2);
+    auto load_q = [&](int buf, int k, int r, uint32_t (&f)[4]) {
+        ldmatrix4(q_lane + buf * (C::kRows * D * 2) + r * (8 * D * 2) + ((2 * k + (lane >> 3)) ^ (lane & 7)) * 16, f);
     };
 
-    // addresses within a stage of this lane's rows of the share's first 16 keys, the swizzle folded in: piece c of a
-    // row's block is at the address ^ 16 c; K's rows are blocks of 8 keys in lanes 0-15 and 16-31 (the lanes' bit 3
-    // chooses the piece of a pair), V's in lanes 0-7 and 8-15 (bit 4)
+    // addresses within a stage of this lane's rows of 16 keys, the swizzle folded in: piece c of a row's block is at
+    // the address ^ 16 c.  K: lanes 0-15 and 16-31 take a pair of pieces of 16 keys.  V, 8-bit: the same (with one
+    // column tile a warp, the piece of two 16 keys); 16-bit (whose blocks of 8 elements are the rows of the product):
+    // lanes 0-7 and 8-15 the pair of pieces, 16-31 the other 8 keys
     constexpr int kMask = C::kBlock == 128 ? 7 : 3, kShift = C::kBlock == 128 ? 0 : 1;
     constexpr int kPieces = C::kBlock / 16;                  // 16-byte pieces of a block
+    constexpr bool kTwoKeys = kE4m3 && C::kCols == 1;
     const uint32_t block_bytes = sub * C::kBlock;            // from one block of a row to the next
-    uint32_t k_lane, v_lane;
-    {
-        const int kr = (lane & 7) + ((lane >> 4) & 1) * 8, vr = (lane & 7) + ((lane >> 3) & 1) * 8;
-        const int kx = ((kr >> kShift) & kMask) ^ ((lane >> 3) & 1), vx = ((vr >> kShift) & kMask) ^ (lane >> 4);
-        k_lane = smem_u32(sm.kv[0]) + kr * C::kBlock + kx * 16;
-        v_lane = smem_u32(sm.kv[0]) + vr * C::kBlock + vx * 16 + kTile * C::kRow;
-    }
     auto key_at = [&](int key) {                             // a multiple of 16 within the tile: 16 keys lie in one box
         return (uint32_t)((key >> ss << ss) * C::kRow + (key & (sub - 1)) * C::kBlock);
     };
-    const int c2 = 2 * (lane & 3), fr = lane >> 2;
+    uint32_t k_lane, v_lane, key16[4];                       // the tile's sixteens of keys
+#pragma unroll
+    for (int j = 0; j < 4; ++j) key16[j] = key_at(min(16 * j + (kTwoKeys ? lane & 16 : 0), kTile - 16));
+    {
+        const int kr = lane & 15, kx = ((kr >> kShift) & kMask) ^ (lane >> 4);
+        const int vr = kE4m3 ? lane & 15 : (lane & 7) + ((lane >> 4) & 1) * 8;
+        const int v_x = ((vr >> kShift) & kMask) ^ (kTwoKeys ? 0 : kE4m3 ? lane >> 4 : (lane >> 3) & 1);
+        k_lane = smem_u32(sm.kv[0]) + key_at(16 * w) + kr * C::kBlock + kx * 16;
+        v_lane = smem_u32(sm.kv[0]) + kTile * C::kRow + vr * C::kBlock + v_x * 16;
+    }
+    const int c2 = 2 * (lane & 3), gr = lane >> 2;           // of an accumulator: its columns (rows of q), its row
     const float sc = a.scale * kLog2e;
     bool ok = true;
 
-    while (left > 0 && ok) {
+    int place = grp, turn = 0;                               // of the group's next tile in the ring: stage and parity
+    for (int seg = 0; left > 0 && ok; ++seg) {
         // ------------------------------------------------------ a head's tiles [tile, tile + cnt)
-        const int cnt = min(left, nt - tile);
+        const int cnt = min(left, nt - tile), buf = seg & 1;
         const int kvh = u / g.row_blocks, row0 = u % g.row_blocks * C::kRows, rows = min(C::kRows, g.rows - row0);
-        // the query rows, 16-byte pieces swizzled by row, a warp per row; for the 8-bit cache as f16 after a power of
-        // two, each 16 elements' pairs in the order 0 2 4 6, 1 3 5 7 (pairs of a quad of bytes go to the halves of k)
-        for (int r = warp; r < C::kRows; r += 8) {
-            uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-            if (r < rows && lane < D / 16) {
-                const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
-                const uint4* src =
-                    reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
-                x = src[2 * lane];
-                y = src[2 * lane + 1];
-            }
-            if constexpr (kE4m3) {
-                const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                uint32_t top = 0u;                           // largest exponent of the row (bits 7..14 of an element)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7F80u, (w[i] >> 16) & 0x7F80u));
-                top = __reduce_max_sync(0xFFFFFFFFu, top) >> 7;
-                // 2^(127 - top); a row of zeros, or with an infinity or NaN, stays as it is
-                const int e = top == 255u || top == 0u ? 127 : min(max(254 - (int)top, 1), 254);
-                const float up = __int_as_float(e << 23);
-                if (lane == 0) sm.q_scale[r] = __int_as_float(max(254 - e, 1) << 23);
-                x = make_uint4(bf16x2_to_f16x2(w[0], up), bf16x2_to_f16x2(w[2], up), bf16x2_to_f16x2(w[4], up),
-                               bf16x2_to_f16x2(w[6], up));
-                y = make_uint4(bf16x2_to_f16x2(w[1], up), bf16x2_to_f16x2(w[3], up), bf16x2_to_f16x2(w[5], up),
-                               bf16x2_to_f16x2(w[7], up));
-            }
-            if (lane < D / 16) {
-                uint8_t* dst = sm.q + r * (D * 2);
-                *reinterpret_cast<uint4*>(dst + ((2 * lane) ^ (r & 7)) * 16) = x;
-                *reinterpret_cast<uint4*>(dst + ((2 * lane + 1) ^ (r & 7)) * 16) = y;
-            }
-        }
-        named_barrier(1, kConsumers);
-        uint32_t qf[C::kQRegs ? D / 16 : 1][4];
+        ok = mbar_wait_live(&sm.q_full[buf], (seg >> 1) & 1, &sm.dead, a.err);
+        uint32_t qf[C::kQRegs ? D / 32 : 1][4];
         if constexpr (C::kQRegs) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) load_q(k, 0, qf[k]);
+            for (int k = 0; k < D / 32; ++k) load_q(buf, 2 * k, 0, qf[k]);
         }
-        // of row tile r, rows lane / 4 (e = 0) and 8 below (e = 1)
-        float o[RT][D / 8][4];
-        float m[RT][2], l[RT][2], qs[RT][2];
-        int lim[RT][2];                                      // keys that the row sees
+        // of row tile r, rows c2 + e of q: outputs transposed, 16 columns a tile; l of the warp's keys
+        float o[NT][C::kCols][4];
+        float m[NT][2], l[NT][2], qs[NT][2];
+        int lim[NT][2];                                      // keys that the row sees
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
+        for (int r = 0; r < NT; ++r) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
+            for (int i = 0; i < C::kCols; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = (set * RT + r) * 16 + fr + 8 * e;
+                const int row = r * 8 + c2 + e;
                 m[r][e] = -CUDART_INF_F, l[r][e] = 0.0f;
-                qs[r][e] = kE4m3 ? sm.q_scale[row] : 1.0f;
+                qs[r][e] = kE4m3 ? sm.q_scale[buf][row] : 1.0f;
                 lim[r][e] = len - a.nq + (row0 + row) / G + 1;
             }
         }
         const int sees_all = len - a.nq + 1;                 // keys below this are seen by every row
 
-        for (int t = (it ^ wg) & 1; t < cnt; t += 2) {
-            const int st = (it + t) % C::kStages;
-            ok = mbar_wait_live(&sm.full[st], ((it + t) / C::kStages) & 1, &sm.dead, a.err);
+        for (int t = (grp + C::kGroups - it % C::kGroups) % C::kGroups; t < cnt; t += C::kGroups) {
+            while (place >= C::kStages) place -= C::kStages, turn ^= 1;
+            const int st = place;
+            place += C::kGroups;
+            ok = ok && mbar_wait_live(&sm.full[st], turn, &sm.dead, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const int share0 = (tile + t) * kTile + split * C::kKeys;   // the share's first key
-            if (share0 + C::kKeys > len) {                   // values past the end may hold NaN, and 0 NaN is NaN
-                for (int i = lane; i < C::kKeys * (C::kRow / 16); i += 32) {
-                    const int key = split * C::kKeys + i / (C::kRow / 16), c = i % (C::kRow / 16);
-                    if ((tile + t) * kTile + key >= len)
-                        *reinterpret_cast<uint4*>(sm.kv[st] + kTile * C::kRow + (key >> ss << ss) * C::kRow +
-                                                  c / kPieces * block_bytes + (key & (sub - 1)) * C::kBlock +
-                                                  c % kPieces * 16) = make_uint4(0u, 0u, 0u, 0u);
+            const int key0 = (tile + t) * kTile + 16 * w;    // the warp's first key
+            if (key0 + 16 > len) {                           // values past the end may hold NaN, and 0 NaN is NaN
+                for (int i = lane; i < C::kRow; i += 32) {
+                    const int key = i / (C::kRow / 16), c = i % (C::kRow / 16);
+                    if (key0 + key >= len)
+                        *reinterpret_cast<uint4*>(sm.kv[st] + kTile * C::kRow + key_at(16 * w) + key * C::kBlock +
+                                                  c / kPieces * block_bytes + c % kPieces * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_shared();                        // before a later load takes their place
-                __syncwarp();
             }
-#pragma unroll 1
-            for (int step = 0; step < C::kKeys / 16; ++step) {
-                const int key0 = share0 + 16 * step;
-                if (key0 >= len) break;
-                const uint32_t k_at = k_lane + st * C::kStage + key_at(split * C::kKeys + 16 * step);
-                const uint32_t v_at = v_lane + st * C::kStage + key_at(split * C::kKeys + 16 * step);
-                // ---- scores: two column tiles of 8 keys per 16
-                // (with one row tile each sum in two halves, so that half as many products wait for one another)
-                float s[RT][2][4], s2[RT][2][4];
+            const uint32_t k_at = k_lane + st * C::kStage;
+            // ---- scores, transposed: 16 keys by 8 query rows a tile
+            // (with one row tile each sum in two halves, so that half as many products wait for one another)
+            float s[NT][4], s2[NT][4];
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < NT; ++r)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                for (int x = 0; x < 4; ++x) s[r][x] = s2[r][x] = 0.0f;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) s[r][i][x] = s2[r][i][x] = 0.0f;
-                constexpr int kPer = kE4m3 ? 2 : 1;              // steps of 16 elements that one load of keys serves
+            for (int k = 0; k < D / 16; k += 2) {
+                uint32_t f[2][4];                            // 16 keys by 16 elements, twice
+                if constexpr (kE4m3) {
+                    uint32_t x[4];
+                    ldmatrix4((k_at + k / kPieces * block_bytes) ^ (k % kPieces * 16), x);
 #pragma unroll
-                for (int k = 0; k < D / 16; k += kPer) {
-                    uint32_t q[RT][kPer][4];
+                    for (int h = 0; h < 2; ++h) {
+                        f[h][0] = e4m3_lo(x[2 * h]), f[h][1] = e4m3_lo(x[2 * h + 1]);
+                        f[h][2] = e4m3_hi(x[2 * h]), f[h][3] = e4m3_hi(x[2 * h + 1]);
+                    }
+                } else {
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                    for (int h = 0; h < 2; ++h) {
+                        const int piece = 2 * (k + h);
+                        ldmatrix4((k_at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16), f[h]);
+                    }
+                }
 #pragma unroll
-                        for (int u = 0; u < kPer; ++u) {
-                            if constexpr (C::kQRegs) {
+                for (int r = 0; r < NT; ++r) {
+                    uint32_t q[4];
+                    if constexpr (C::kQRegs) {
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) q[r][u][x] = qf[k + u][x];
-                            } else {
-                                load_q(k + u, r, q[r][u]);
-                            }
+                        for (int x = 0; x < 4; ++x) q[x] = qf[k / 2][x];
+                    } else {
+                        load_q(buf, k, r, q);
+                    }
+                    mma_16816<kE4m3>(s[r], f[0], q[0], q[1]);
+                    mma_16816<kE4m3>(NT == 1 ? s2[r] : s[r], f[1], q[2], q[3]);
+                }
+            }
+            // ---- scales, and keys that a row does not see: this lane's keys are key0 + gr and 8 on
+            float ks[2] = {sc, sc}, vs[2], lv[2];            // the values' scales and their logarithms
+            const bool masked = key0 + 16 > sees_all;
+            if constexpr (kE4m3) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float* p = &sm.scale[st][16 * w + gr + 8 * h];
+                    ks[h] = p[0] * sc;
+                    vs[h] = key0 + gr + 8 * h < len ? p[kTile] : 0.0f;   // scales past the end may be anything
+                    lv[h] = fmaxf(lg2(vs[h]), kLeast);
+                }
+            }
+            bool grow = false;
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[h] = NT == 1 ? s[r][2 * h + e] + s2[r][2 * h + e] : s[r][2 * h + e];
+                        x[h] *= ks[h] * qs[r][e];
+                        if (masked && key0 + gr + 8 * h >= lim[r][e]) x[h] = -CUDART_INF_F;
+                        s[r][2 * h + e] = x[h];
+                    }
+                    grow = grow || (kE4m3 ? fmaxf(x[0] + lv[0], x[1] + lv[1]) : fmaxf(x[0], x[1])) > m[r][e] + kGrow;
+                }
+            // ---- running maximum: exchanged only where some score of the group has grown past it.  This barrier also
+            // says that the group is done with the probabilities of its tile before, and the next with these zeros
+            if (named_barrier_or(2 + grp, 128, grow || !ok)) {
+                if (!named_barrier_and(2 + grp, 128, ok)) {  // all leave if one gave up
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = kE4m3 ? fmaxf(s[r][e] + lv[0], s[r][2 + e] + lv[1]) : fmaxf(s[r][e], s[r][2 + e]);
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+                        if (gr == 0) sm.top[grp][w][r * 8 + c2 + e] = x;
+                    }
+                named_barrier(2 + grp, 128);
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = r * 8 + c2 + e;
+                        const float x = fmaxf(fmaxf(sm.top[grp][0][row], sm.top[grp][1][row]),
+                                              fmaxf(sm.top[grp][2][row], sm.top[grp][3][row]));
+                        if (x > m[r][e] + kGrow) {
+                            const float f = ex2(m[r][e] - x);
+                            m[r][e] = x;
+                            l[r][e] *= f;
+#pragma unroll
+                            for (int i = 0; i < C::kCols; ++i) o[r][i][e] *= f, o[r][i][2 + e] *= f;
                         }
-                    const int piece = kE4m3 ? k : 2 * k;         // and the next
-                    {
-                        uint32_t f[4];
-                        ldmatrix4((k_at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16), f);
+                    }
+            }
+            // ---- probabilities, transposed into the second product's columns
+#pragma unroll
+            for (int r = 0; r < NT; ++r) {
+                const float n0 = m[r][0] == -CUDART_INF_F ? 0.0f : m[r][0];
+                const float n1 = m[r][1] == -CUDART_INF_F ? 0.0f : m[r][1];
+                uint32_t pb[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x0 = ex2(s[r][2 * h] - n0), x1 = ex2(s[r][2 * h + 1] - n1);
+                    l[r][0] += x0;
+                    l[r][1] += x1;
+                    if (kE4m3) x0 *= vs[h], x1 *= vs[h];
+                    pb[h] = movmatrix_t(pack_p<kE4m3>(x0, x1));
+                }
+                sm.p[grp][w][r][lane] = make_uint2(pb[0], pb[1]);
+            }
+            named_barrier(2 + grp, 128);
+            // ---- O^T += V^T P^T, the tile's 64 keys by the warp's columns
+            const uint32_t v_at = v_lane + st * C::kStage;
+            if constexpr (kTwoKeys) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {             // lanes 16-31 read the second 16 keys
+                    uint32_t x[4], f[2][4];
+                    ldmatrix4_t((v_at + key16[j]) ^ (w * 16), x);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) v_rows(x[2 * h], x[2 * h + 1], f[h]);
+#pragma unroll
+                    for (int r = 0; r < NT; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint2 p = sm.p[grp][j + h][r][lane];
+                            mma_16816<true>(o[r][0], f[h], p.x, p.y);
+                        }
+                }
+            } else {
+                constexpr int kPer = kE4m3 ? 2 : 1;          // column tiles that one load serves
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t f[C::kCols][4];
+                    const uint32_t at = v_at + key16[j];
+#pragma unroll
+                    for (int i = 0; i < C::kCols; i += kPer) {
+                        const int piece = (kE4m3 ? 1 : 2) * (w * C::kCols + i);
+                        const uint32_t from = (at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16);
                         if constexpr (kE4m3) {
-                            const uint32_t x[8] = {e4m3_lo(f[0]), e4m3_hi(f[0]), e4m3_lo(f[1]), e4m3_hi(f[1]),
-                                                   e4m3_lo(f[2]), e4m3_hi(f[2]), e4m3_lo(f[3]), e4m3_hi(f[3])};
-#pragma unroll
-                            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const uint32_t(&y)[4] = q[r][u % kPer];
-                                    auto& z = RT == 1 && u ? s2 : s;
-                                    mma_f16_16816(z[r][0], y[0], y[1], y[2], y[3], x[2 * u], x[2 * u + 1]);
-                                    mma_f16_16816(z[r][1], y[0], y[1], y[2], y[3], x[4 + 2 * u], x[5 + 2 * u]);
-                                }
+                            uint32_t x[4];
+                            ldmatrix4_t(from, x);
+                            v_rows(x[0], x[1], f[i]);
+                            v_rows(x[2], x[3], f[i + 1 < C::kCols ? i + 1 : i]);
                         } else {
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const uint32_t(&y)[4] = q[r][0];
-                                auto& z = RT == 1 && (k & 1) ? s2 : s;
-                                mma_bf16_16816(z[r][0], y[0], y[1], y[2], y[3], f[0], f[1]);
-                                mma_bf16_16816(z[r][1], y[0], y[1], y[2], y[3], f[2], f[3]);
-                            }
+                            ldmatrix4_t(from, f[i]);
                         }
                     }
-                }
-                // ---- scales, and keys that a row does not see
-                float2 vs[2], lv[2];           // the values' scales and their logarithms
-                const bool masked = key0 + 16 > sees_all;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float2 ks = make_float2(sc, sc);
-                    const int key = key0 + 8 * i + c2;
-                    if constexpr (kE4m3) {
-                        const float* p = &sm.scale[st][split * C::kKeys + 16 * step + 8 * i + c2];
-                        const float2 u = *reinterpret_cast<const float2*>(p);
-                        vs[i] = *reinterpret_cast<const float2*>(p + kTile);
-                        ks = make_float2(u.x * sc, u.y * sc);
-                        if (key >= len) vs[i].x = 0.0f;            // scales past the end may be anything
-                        if (key + 1 >= len) vs[i].y = 0.0f;
-                        lv[i] = make_float2(fmaxf(lg2(vs[i].x), kLeast), fmaxf(lg2(vs[i].y), kLeast));
-                    }
+                    for (int r = 0; r < NT; ++r) {
+                        const uint2 p = sm.p[grp][j][r][lane];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            s[r][i][x] = (RT == 1 ? s[r][i][x] + s2[r][i][x] : s[r][i][x]) * ((x & 1 ? ks.y : ks.x) * qs[r][x >> 1]);
-                        if (masked) {
-                            if (key >= lim[r][0]) s[r][i][0] = -CUDART_INF_F;
-                            if (key + 1 >= lim[r][0]) s[r][i][1] = -CUDART_INF_F;
-                            if (key >= lim[r][1]) s[r][i][2] = -CUDART_INF_F;
-                            if (key + 1 >= lim[r][1]) s[r][i][3] = -CUDART_INF_F;
-                        }
-                    }
-                }
-                // ---- running maximum
-                float top[RT][2];
-                bool grow = false;
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    float t0 = -CUDART_INF_F, t1 = t0;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (kE4m3) {
-                            t0 = fmaxf(t0, fmaxf(s[r][i][0] + lv[i].x, s[r][i][1] + lv[i].y));
-                            t1 = fmaxf(t1, fmaxf(s[r][i][2] + lv[i].x, s[r][i][3] + lv[i].y));
-                        } else {
-                            t0 = fmaxf(t0, fmaxf(s[r][i][0], s[r][i][1]));
-                            t1 = fmaxf(t1, fmaxf(s[r][i][2], s[r][i][3]));
-                        }
-                    }
-                    t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 1));
-                    t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 1));
-                    top[r][0] = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, 2));
-                    top[r][1] = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, 2));
-                    grow = grow || top[r][0] > m[r][0] + kGrow || top[r][1] > m[r][1] + kGrow;
-                }
-                if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (top[r][e] > m[r][e] + kGrow) {
-                                const float f = ex2(m[r][e] - top[r][e]);
-                                m[r][e] = top[r][e];
-                                l[r][e] *= f;
-#pragma unroll
-                                for (int i = 0; i < D / 8; ++i) o[r][i][2 * e] *= f, o[r][i][2 * e + 1] *= f;
-                            }
-                }
-                // ---- probabilities, as the second product's rows
-                uint32_t pa[RT][4];
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const float n0 = m[r][0] == -CUDART_INF_F ? 0.0f : m[r][0], n1 = m[r][1] == -CUDART_INF_F ? 0.0f : m[r][1];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x0 = ex2(s[r][i][0] - n0), x1 = ex2(s[r][i][1] - n0);
-                        float x2 = ex2(s[r][i][2] - n1), x3 = ex2(s[r][i][3] - n1);
-                        l[r][0] += x0 + x1;
-                        l[r][1] += x2 + x3;
-                        if (kE4m3) x0 *= vs[i].x, x1 *= vs[i].y, x2 *= vs[i].x, x3 *= vs[i].y;
-                        pa[r][2 * i] = pack_p<kE4m3>(x0, x1);
-                        pa[r][2 * i + 1] = pack_p<kE4m3>(x2, x3);
-                    }
-                }
-                // ---- O += P V
-                {
-#pragma unroll
-                    for (int p = 0; p < C::kRow / 32; ++p) {
-                        const int piece = 2 * p;
-                        uint32_t f[4];
-                        ldmatrix4_t((v_at + piece / kPieces * block_bytes) ^ (piece % kPieces * 16), f);
-                        if constexpr (kE4m3) {
-                            // the bytes of a key pair: even elements of both keys, then odd ones
-                            const uint32_t e0 = prmt(f[0], 0u, 0x3120), e1 = prmt(f[1], 0u, 0x3120);
-                            const uint32_t e2 = prmt(f[2], 0u, 0x3120), e3 = prmt(f[3], 0u, 0x3120);
-                            const uint32_t v[8] = {e4m3_lo(e0), e4m3_lo(e1), e4m3_hi(e0), e4m3_hi(e1),
-                                                   e4m3_lo(e2), e4m3_lo(e3), e4m3_hi(e2), e4m3_hi(e3)};
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const uint32_t(&x)[4] = pa[r];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    mma_f16_16816(o[r][4 * p + u], x[0], x[1], x[2], x[3], v[2 * u], v[2 * u + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                const uint32_t(&x)[4] = pa[r];
-                                mma_bf16_16816(o[r][2 * p], x[0], x[1], x[2], x[3], f[0], f[1]);
-                                mma_bf16_16816(o[r][2 * p + 1], x[0], x[1], x[2], x[3], f[2], f[3]);
-                            }
-                        }
+                        for (int i = 0; i < C::kCols; ++i) mma_16816<kE4m3>(o[r][i], f[i], p.x, p.y);
                     }
                 }
             }
@@ -602,68 +641,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&sm.empty[st]);
         }
 
-        // ------------------------------------------------------ the shares joined: maxima and sums first
+        // ------------------------------------------------------ the groups joined
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < NT; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                l[r][e] += __shfl_xor_sync(0xFFFFFFFFu, l[r][e], 1);
-                l[r][e] += __shfl_xor_sync(0xFFFFFFFFu, l[r][e], 2);
-                if ((lane & 3) == 0) {
-                    float* p = sm.ml[share][(set * RT + r) * 16 + fr + 8 * e];
-                    p[0] = m[r][e], p[1] = l[r][e];
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) l[r][e] += __shfl_xor_sync(0xFFFFFFFFu, l[r][e], x);
+                if (gr == 0) {
+                    sm.l[grp][w][r * 8 + c2 + e] = l[r][e];
+                    if (w == 0) sm.m[grp][r * 8 + c2 + e] = m[r][e];
                 }
             }
         ok = named_barrier_and(1, kConsumers, ok);           // all leave if one gave up
+        if (tid == 0) mbar_arrive(&sm.q_empty[buf]);
+        float f[NT][2];
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < NT; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = (set * RT + r) * 16 + fr + 8 * e;
-                float M = -CUDART_INF_F, L = 0.0f;
+                const int row = r * 8 + c2 + e;
+                float M = -CUDART_INF_F;
 #pragma unroll
-                for (int i = 0; i < C::kShares; ++i) M = fmaxf(M, sm.ml[i][row][0]);
-#pragma unroll
-                for (int i = 0; i < C::kShares; ++i) {
-                    const float x = sm.ml[i][row][0], y = sm.ml[i][row][1];
-                    L += x == -CUDART_INF_F ? y : y * ex2(x - M);   // a share that sees no key holds 0, or a NaN
-                }
-                const float f = m[r][e] == -CUDART_INF_F ? 1.0f : ex2(m[r][e] - M);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[r][i][2 * e] *= f, o[r][i][2 * e + 1] *= f;
-                if (share == 0 && (lane & 3) == 0) sm.fin[row][0] = M, sm.fin[row][1] = L;
+                for (int i = 0; i < C::kGroups; ++i) M = fmaxf(M, sm.m[i][row]);
+                f[r][e] = m[r][e] == -CUDART_INF_F ? 1.0f : ex2(m[r][e] - M);   // a group that sees no key holds 0, or NaN
             }
-        // outputs: a round each share adds another piece of its columns, so that all work and the order is fixed
-        constexpr int kPairs = D / 16, kPcs = C::kShares < kPairs ? C::kShares : kPairs, kPer2 = kPairs / kPcs;
+        for (int row = tid; row < C::kRows; row += kConsumers) {
+            float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C::kGroups; ++i) M = fmaxf(M, sm.m[i][row]);
+#pragma unroll
+            for (int i = 0; i < C::kGroups; ++i) {
+                const float x = sm.m[i][row], y = (sm.l[i][0][row] + sm.l[i][1][row]) + (sm.l[i][2][row] + sm.l[i][3][row]);
+                L += x == -CUDART_INF_F ? y : y * ex2(x - M);
+            }
+            sm.fin[row][0] = M, sm.fin[row][1] = L;
+        }
+        // one group after the other adds its outputs
 #pragma unroll 1
-        for (int round = 0; round < C::kShares; ++round) {
-            const int piece = (share + round) % C::kShares;
+        for (int round = 0; round < C::kGroups; ++round) {
+            if (round == grp) {
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) {
-                if (i / kPer2 != piece) continue;
+                for (int r = 0; r < NT; ++r)
 #pragma unroll
-                for (int re = 0; re < 2 * RT; ++re) {
-                    const int r = re >> 1, e = re & 1;
-                    float* dst = sm.acc[(set * RT + r) * 16 + fr + 8 * e] + 16 * i;
-                    const float* x = &o[r][2 * i][2 * e];
-                    const float* y = &o[r][2 * i + 1][2 * e];
-                    if constexpr (kE4m3) {                   // columns 4 c .. + 3: even and odd tiles interleave
-                        float4 v = make_float4(x[0], y[0], x[1], y[1]);
-                        if (round > 0) {
-                            const float4 w = *reinterpret_cast<float4*>(dst + 2 * c2);
-                            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < C::kCols; ++i) {
+                            float* dst = sm.acc[r * 8 + c2 + e] + 16 * (w * C::kCols + i);
+                            float x = o[r][i][e] * f[r][e], y = o[r][i][2 + e] * f[r][e];
+                            if constexpr (kE4m3) {           // rows 0-7 of a tile are the even elements
+                                float2* at = reinterpret_cast<float2*>(dst + 2 * gr);
+                                if (round > 0) x += at->x, y += at->y;
+                                *at = make_float2(x, y);
+                            } else {
+                                if (round > 0) x += dst[gr], y += dst[gr + 8];
+                                dst[gr] = x, dst[gr + 8] = y;
+                            }
                         }
-                        *reinterpret_cast<float4*>(dst + 2 * c2) = v;
-                    } else {
-                        float2 v = make_float2(x[0], x[1]), w = make_float2(y[0], y[1]);
-                        if (round > 0) {
-                            const float2 p = *reinterpret_cast<float2*>(dst + c2), q = *reinterpret_cast<float2*>(dst + 8 + c2);
-                            v.x += p.x, v.y += p.y, w.x += q.x, w.y += q.y;
-                        }
-                        *reinterpret_cast<float2*>(dst + c2) = v;
-                        *reinterpret_cast<float2*>(dst + 8 + c2) = w;
-                    }
-                }
             }
             named_barrier(1, kConsumers);
         }
@@ -802,7 +836,7 @@ DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     g.page_shift = 4;
     while (1 << g.page_shift < c.page_size) ++g.page_shift;
     g.rows = c.q_heads / c.kv_heads * nq;
-    g.row_pad = 16 * row_tiles(g.rows, c.head_dim);
+    g.row_pad = 8 * row_tiles(g.rows, c.head_dim);
     g.row_blocks = (g.rows + g.row_pad - 1) / g.row_pad;
     g.units = c.kv_heads * g.row_blocks;
     // one block a multiprocessor, no more than the longest lengths give work to
@@ -813,9 +847,9 @@ DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     return g;
 }
 
-template <int D, bool kE4m3, int MT>
+template <int D, bool kE4m3, int NT>
 cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStream_t st) {
-    using C = Cfg<D, kE4m3, MT>;
+    using C = Cfg<D, kE4m3, NT>;
     const int64_t rows = (int64_t)a.cache.num_pages * a.c.kv_heads * a.c.page_size;
     const int sub = std::min(a.c.page_size, kTile);
     CUtensorMap km, vm;
@@ -823,24 +857,25 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
         !make_row_blocks_map(&vm, a.cache.v, rows, C::kRow, C::kRow, C::kBlock, sub, C::kRow / C::kBlock))
         return cudaErrorInvalidValue;
     static int done[64] = {0};
-    const int smem = (int)sizeof(Smem<D, kE4m3, MT>) + 1024;
-    static_assert(sizeof(Smem<D, kE4m3, MT>) + 1024 <= 232448 && C::kStages >= 2, "shared memory per block");
-    cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, MT>, smem, done);
+    const int smem = (int)sizeof(Smem<D, kE4m3, NT>) + 1024;
+    static_assert(sizeof(Smem<D, kE4m3, NT>) + 1024 <= 232448 && C::kStages >= 2, "shared memory per block");
+    cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, NT>, smem, done);
     if (ce != cudaSuccess) return ce;
-    ce = launch_pdl(k_attn_decode<D, kE4m3, MT>, dim3(g.blocks), dim3(kThreads), (size_t)smem, st, km, vm, a, g);
+    ce = launch_pdl(k_attn_decode<D, kE4m3, NT>, dim3(g.blocks), dim3(C::kThreads), (size_t)smem, st, km, vm, a, g);
     if (ce != cudaSuccess || g.blocks == 1) return ce;
-    return launch_pdl(k_attn_combine<D>, dim3(g.blocks - 1, 4), dim3(256), 0, st, a, g);
+    return launch_pdl(k_attn_combine<D>, dim3(g.blocks - 1, 16), dim3(256), 0, st, a, g);
 }
 
 template <int D, bool kE4m3>
 cudaError_t decode_rows(const AttnDecodeArgs& a, cudaStream_t st) {
     const DecodeGrid g = decode_grid(a.c, a.B, a.nq, a.max_len);
     switch (g.row_pad) {
-        case 16: return decode_launch<D, kE4m3, 1>(a, g, st);
-        case 32: return decode_launch<D, kE4m3, 2>(a, g, st);
+        case 8: return decode_launch<D, kE4m3, 1>(a, g, st);
+        case 16: return decode_launch<D, kE4m3, 2>(a, g, st);
+        case 32: return decode_launch<D, kE4m3, 4>(a, g, st);
         default:
             if constexpr (D == 256) return cudaErrorInvalidValue;
-            else return decode_launch<D, kE4m3, 4>(a, g, st);
+            else return decode_launch<D, kE4m3, 8>(a, g, st);
     }
 }
 

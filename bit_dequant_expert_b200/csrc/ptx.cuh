@@ -154,6 +154,17 @@ __device__ __forceinline__ bool named_barrier_and(uint32_t id, uint32_t nthreads
     return r != 0;
 }
 
+// Named barrier that also ORs a predicate over its threads.
+__device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t nthreads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
 // Signals arrival at a named barrier without waiting for it.
 __device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -203,6 +214,13 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t saddr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(saddr)
                  : "memory");
+}
+
+// An 8x8 block of 16-bit elements, transposed across the warp.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t v) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
 }
 
 // 2^x, the hardware's approximation (relative error about 2^-22).
