@@ -12,6 +12,12 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+__device__ __forceinline__ uint32_t dynamic_smem_bytes() {
+    uint32_t n;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
+    return n;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -294,13 +300,41 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
         : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc].
-__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc] and A[tmem] * B[smem desc], for a
+// whole warp in step of which one lane issues: predicated instead of branched,
+// so that the operands, the same in all lanes, stay in uniform registers.  The
+// descriptors come as low words (start address and leading offset) and one
+// constant high word: a step along K adds a constant to a low word.
+__device__ __forceinline__ void tc_mma_ss_warp(bool issue, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                               uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, i;\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 i, %6, 0;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_warp(bool issue, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                               uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, i;\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 i, %6, 0;\n\t"
+        "@i tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_warp(bool issue, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred i;\n\tsetp.ne.b32 i, %1, 0;\n\t"
+        "@i tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((uint32_t)issue)
         : "memory");
 }
 
@@ -366,17 +400,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
     return d;
 }
 
-// The same swizzled layout for an operand whose contiguous dimension is M or
-// N: panels of 64 elements (128 bytes) x rows along K, 8 rows to a 1024-byte
-// group, the next panel panel_bytes on.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t saddr, uint32_t panel_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(panel_bytes >> 4) << 16;          // leading byte offset: next panel
-    d |= (uint64_t)(1024 >> 4) << 32;                 // stride byte offset: next 8 rows along K
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// The descriptor's words: the high one, the same for every operand in this
+// layout, and the low one.  An operand whose contiguous dimension is M or N
+// lies in panels of 64 elements (128 bytes) x rows along K, 8 rows to a
+// 1024-byte group, the next panel `panel` bytes on (K-major operands: 0).
+__host__ __device__ constexpr uint32_t smem_desc_hi() { return (1024u >> 4) | 1u << 14 | 2u << 29; }
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t saddr, uint32_t panel) {
+    return ((saddr & 0x3FFFFu) >> 4) | (panel >> 4) << 16;
 }
 
 // Instruction descriptor, kind::f16: bf16 A and B (both K-major), fp32 D.
