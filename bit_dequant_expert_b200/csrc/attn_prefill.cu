@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_commit_warp(issue, &sm.s_full[buf]);
                 };
-                // O `s` += P V, P in bf16 over the S buffer
+                // O `s` += P V, P in bf16 over the S buffer: each half of the keys over its own scores
                 auto product_o = [&](int s, int buf, int first, bool add) {
                     constexpr int kKeys = kN / C::kParts;
                     const uint32_t d = tmem + C::kOCol + s * D, pa = tmem + buf * kN;
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vb[p] = slot_lo + (first + p) % C::kSlots * (C::kSlot / 16) + smem_desc_lo(0, kKeys * 128);
 #pragma unroll
                     for (int kk = 0; kk < kN / 16; ++kk)
-                        tc_mma_ts_warp(issue, d, pa + kk * 8, vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi,
+                        tc_mma_ts_warp(issue, d, pa + kk / 4 * 64 + kk % 4 * 8, vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi,
                                        kIdO, add || kk != 0);
                     tc_commit_warp(issue, &sm.o_done[s]);
                 };
@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = kMode == kPairs ? grp : 0;                // query tile
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
         const uint32_t s_addr = lane_base + grp * kN + half * 64;
-        const uint32_t p_addr = lane_base + grp * kN + half * 32;
+        const uint32_t p_addr = s_addr;                         // P over this half's own scores
+        const uint32_t pair = 1 + grp * 4 + (warp & 3);         // barrier of the two warps that share rows
         const uint32_t o_addr = lane_base + C::kOCol + (kMode == kTurns ? 0 : grp * D);
         const int r = (warp & 3) * 32 + lane;                   // row within the tile
         const int row = (s ? w.row[1] : w.row[0]) + r;          // row within the sequence
@@ -451,31 +452,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float t0 = -CUDART_INF_F, t1 = t0, t2 = t0, t3 = t0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                t0 = fmaxf(t0, __uint_as_float(x[0][i]));
-                t1 = fmaxf(t1, __uint_as_float(x[0][16 + i]));
-                t2 = fmaxf(t2, __uint_as_float(x[1][i]));
-                t3 = fmaxf(t3, __uint_as_float(x[1][16 + i]));
+            for (int i = 0; i < 16; i += 2) {
+                t0 = max3(t0, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
+                t1 = max3(t1, __uint_as_float(x[0][16 + i]), __uint_as_float(x[0][17 + i]));
+                t2 = max3(t2, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
+                t3 = max3(t3, __uint_as_float(x[1][16 + i]), __uint_as_float(x[1][17 + i]));
             }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * sc;
+            const float top = fmaxf(max3(t0, t1, t2), t3) * sc;
             if (kMode == kTurns && j > 0) {                     // the maximum as the other group left it
                 ok = ok && mbar_wait_live(&sm.m_full[grp ^ 1], ((j - 1) >> 1) & 1, &sm.dead, a.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 m = sm.m[grp ^ 1][r];
             }
-            // This barrier also says that both halves have read their scores: P may take their place.
-            if (named_barrier_or(1 + grp, 256, top > m + kGrow || !ok)) {
-                if (!named_barrier_and(1 + grp, 256, ok)) {     // all leave if one gave up
+            // a row's two threads (and their warps) agree whether its maximum has to move
+            if (named_barrier_or(pair, 64, top > m + kGrow || !ok)) {
+                if (!named_barrier_and(pair, 64, ok)) {     // all leave if one gave up
                     ok = false;
                     break;
                 }
                 if (half == 1) sm.top[grp][r] = top;
-                named_barrier(1 + grp, 256);
+                named_barrier(pair, 64);
                 if (half == 0) {
                     const float t = fmaxf(top, sm.top[grp][r]);
                     sm.m[grp][r] = t > m + kGrow ? t : m;
                 }
-                named_barrier(1 + grp, 256);
+                named_barrier(pair, 64);
                 const float mn = sm.m[grp][r];
                 const float f = mn == m ? 1.0f : ex2(m - mn);
                 if (kMode != kTurns) l *= f;
@@ -499,27 +500,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m_own = m;
             }
             const float neg = m == -CUDART_INF_F ? 0.0f : -m;
-            float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+            const uint64_t sc2 = pack_f32x2(sc, sc), neg2 = pack_f32x2(neg, neg);
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-            uint32_t p[16];
+                uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const uint32_t* y = &x[h][2 * i];
-                const float p0 = ex2(fmaf(__uint_as_float(y[0]), sc, neg));
-                const float p1 = ex2(fmaf(__uint_as_float(y[1]), sc, neg));
-                const float p2 = ex2(fmaf(__uint_as_float(y[2]), sc, neg));
-                const float p3 = ex2(fmaf(__uint_as_float(y[3]), sc, neg));
-                s0 += p0;
-                s1 += p1;
-                s2 += p2;
-                s3 += p3;
-                p[i] = pack_bf16x2(p0, p1);
-                p[i + 1] = pack_bf16x2(p2, p3);
+                for (int i = 0; i < 16; ++i) {
+                    uint64_t y = fma_f32x2(pack_f32x2(__uint_as_float(x[h][2 * i]), __uint_as_float(x[h][2 * i + 1])), sc2, neg2);
+                    float lo, hi;
+                    unpack_f32x2(y, lo, hi);
+                    lo = ex2(lo), hi = ex2(hi);
+                    sum[i & 1] = add_f32x2(sum[i & 1], pack_f32x2(lo, hi));
+                    p[i] = pack_bf16x2(lo, hi);
+                }
+                tmem_st16(p_addr + 16 * h, p);
             }
-            tmem_st16(p_addr + 16 * h, p);
+            {
+                float lo, hi;
+                unpack_f32x2(add_f32x2(sum[0], sum[1]), lo, hi);
+                l += lo + hi;
             }
-            l += (s0 + s1) + (s2 + s3);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -535,17 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = sm.m[last][r];
             if (m != m_own) l *= ex2(m_own - m);
         }
-        if (kMode == kTurns) named_barrier(3, 512); else named_barrier(1 + grp, 256);   // all have read it
+        if (kMode == kTurns) named_barrier(15, 512); else named_barrier(pair, 64);   // all have read it
         (half ? sm.top : sm.m)[grp][r] = l;
-        if (kMode == kTurns) named_barrier(3, 512); else named_barrier(1 + grp, 256);
+        if (kMode == kTurns) named_barrier(15, 512); else named_barrier(pair, 64);
         l = sm.m[grp][r] + sm.top[grp][r];
         float m1 = m, f = 1.0f, f1 = 1.0f;                      // the row's maximum of all, the groups' factors
         if (kMode == kTurns) {
             l += sm.m[grp ^ 1][r] + sm.top[grp ^ 1][r];
         } else if (kMode == kHalves) {
-            named_barrier(3, 512);
+            named_barrier(15, 512);
             if (half) sm.top[grp][r] = l; else sm.m[grp][r] = m;
-            named_barrier(3, 512);
+            named_barrier(15, 512);
             const float mo = sm.m[grp ^ 1][r], lo = sm.top[grp ^ 1][r];
             m1 = fmaxf(m, mo);
             f = m == -CUDART_INF_F ? 1.0f : ex2(m - m1);        // a group that sees no key holds 0, or NaN
