@@ -13,6 +13,7 @@
 // stores whole 128-byte lines; the angles of a block's tokens are formed once
 // for all heads in shared memory.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.h"
 #include "common.cuh"
@@ -23,7 +24,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokMax = 8;        // tokens per block of the prepare kernel
+constexpr int kRows = 4;          // heads a lane of the prepare kernel has in flight
+constexpr int kPrepare = 128;     // its threads a block
 constexpr float kE4m3Max = 448.0f;
 
 // (lo, hi) -> two e4m3 codes, rounded to nearest even, the magnitude limited to 448.
@@ -104,96 +106,162 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float s) {
     return w;
 }
 
-template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) k_attn_prepare(const AttnPrepareArgs a, int tok_per_block) {
-    constexpr int L = D / 8, kGroups = kThreads / L;
-    __shared__ float2 trig[kTokMax][D / 2];   // (cos, sin) of the block's tokens
+// Runs of heads that a warp of the prepare kernel takes.
+enum Kind { kQuery, kKey, kValue };
+
+// A warp takes a token's heads (or a part of them), D / 8 lanes a head and
+// kRows heads a lane at once, all of whose loads are on the way together.  Of
+// a pair's elements a, b (weights w_a, w_b) the rotated ones are
+//   inv (a (c w_a) - b (s w_b))  and  inv (b (c w_b) + a (s w_a)),
+// inv the root's reciprocal: the products in brackets are the same for all of
+// the token's heads and stay in registers, so that a head takes two products
+// and a scaling an element (in pairs of fp32, one instruction for two).  With
+// a lane's place in the token's heads, the kind of head and the angles worked
+// out anew for each row the kernel was bound by its instructions (16384 tokens
+// of 20 heads of 128: 250 instructions a warp and 2 rows, 48 us).
+template <int D, bool kE4m3, bool kHalf>
+__global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareArgs a, int parts, int page_shift) {
+    constexpr int L = D / 8, R = 32 / L;
+    __shared__ __align__(16) float2 trig[kPrepare / 32][D / 2];   // (cos, sin) of a warp's token
     griddep_launch_dependents();
     griddep_wait();
-    const int t0 = blockIdx.x * tok_per_block;
-    const int nt = min(tok_per_block, a.T - t0);
-    const int half = a.rot_dim / 2;
-    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        // angle in half turns: x = pos f / pi, less the nearest even whole number
-        double x = (double)a.positions[t0 + t] * (double)a.inv_freq[p] * 0.31830988618379067154;
-        x -= 2.0 * rint(0.5 * x);
-        float s, c;
-        sincospif((float)x, &s, &c);
-        trig[t][p] = make_float2(c * a.rope_scale, s * a.rope_scale);
-    }
-    __syncthreads();
-    const int l = threadIdx.x % L, g = threadIdx.x / L;
-    const int Hq = a.c.q_heads, Hk = a.c.kv_heads, H = Hq + 2 * Hk;
-    const int rows = nt * H;
-    // every lane of a warp takes part in the shuffles: groups past the end work on the last row
-    for (int base = 0; base < rows; base += kGroups) {
-        const bool live = base + g < rows;
-        const int r = live ? base + g : rows - 1;
-        const int t = r / H, h = r - t * H;
-        const int64_t tok = t0 + t;
-        float f[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.qkv + tok * a.qkv_stride + (int64_t)h * D) + l), f);
-        const bool is_v = h >= Hq + Hk;
-        const uint16_t* w = h < Hq ? a.q_weight : a.k_weight;
-        float ss = 0.0f;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % L, sub = lane / L;
+    const int64_t unit = (int64_t)blockIdx.x * (kPrepare / 32) + warp;
+    const int64_t tok = unit / parts;
+    if (tok >= a.T) return;
+    const int part = (int)(unit - tok * parts);
+    const int Hq = a.c.q_heads, Hk = a.c.kv_heads, H = Hq + 2 * Hk, half = a.rot_dim / 2;
+    const int lo = H * part / parts, hi = H * (part + 1) / parts;
+    const uint4* src = reinterpret_cast<const uint4*>(a.qkv + tok * a.qkv_stride) + l;
+
+    // a batch of rows, heads [b, end): each is loaded while the one before it is worked on, across the kinds of heads
+    uint4 in[kRows];
+    auto load = [&](int b, int end) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-        ss = group_sum<L>(ss);
-        if (!is_v && w) {
-            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-            float wf[8];
-            unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), wf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * wf[e];
+        for (int n = 0; n < kRows; ++n) {
+            const int h = b + n * R + sub;
+            in[n] = h < end ? __ldg(src + h * L) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (half) {
-            if (a.layout == ATTN_ROPE_HALF) {
-                // the other element of a pair is half / 8 lanes away
-                const int hl = half >> 3;
-                const int other = (l < hl ? l + hl : l - hl) & (L - 1);
-                const int p0 = (l < hl ? l : l - hl) * 8;
-                float o[8];
+    };
+    // the first head of each kind in the warp's part, and its end (none: equal)
+    const int k0 = max(lo, Hq), k1 = max(k0, min(hi, Hq + Hk)), v0 = max(lo, Hq + Hk), v1 = max(v0, hi);
+    const int q1 = max(lo, min(hi, Hq));
+    load(lo < q1 ? lo : k0 < k1 ? k0 : v0, lo < q1 ? q1 : k0 < k1 ? k1 : v1);
+
+    int64_t row = -1;                                            // of the token in the cache, head 0
+    if (a.slots && hi > Hq) {
+        const int slot = __ldg(a.slots + tok), page = slot >> page_shift;
+        if (slot >= 0 && page < a.cache.num_pages)
+            row = ((int64_t)page * Hk << page_shift) + (slot & ((1 << page_shift) - 1));
+        else if (slot >= 0 && lane == 0)
+            set_error(a.err, MOE_ERR_BOUNDS);
+    }
+    if (half && lo < Hq + Hk) {
+        const double pos = (double)__ldg(a.positions + tok) * 0.31830988618379067154;
+        for (int p = lane; p < half; p += 32) {
+            // angle in half turns: x = pos f / pi, less the nearest even whole number
+            double x = pos * (double)__ldg(a.inv_freq + p);
+            x -= 2.0 * rint(0.5 * x);
+            float s, c;
+            sincospif((float)x, &s, &c);
+            trig[warp][p] = make_float2(c * a.rope_scale, s * a.rope_scale);
+        }
+        __syncwarp();
+    }
+    const int hl = half >> 3;                                    // lanes of the first elements of halves' pairs
+    const bool turned = l * 8 < a.rot_dim, low = l < hl;
+    const int other = kHalf && turned ? (low ? l + hl : l - hl) : l;   // the lane of the pairs' other elements
+
+    auto run = [&](auto kind, int beg, int end, int next, int next_end) {
+        constexpr int kKind = decltype(kind)::value;
+        uint64_t A[4], B[4];                                     // factors of an element and of its pair's other one
+        const uint16_t* w = kKind == kQuery ? a.q_weight : a.k_weight;
+        if constexpr (kKind != kValue) {
+            float wf[8], wo[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xFFFFFFFFu, f[e], other, L);
-                if (!is_v && l < 2 * hl) {
+            for (int e = 0; e < 8; ++e) wf[e] = wo[e] = 1.0f;
+            if (w) {
+                unpack8(__ldg(reinterpret_cast<const uint4*>(w) + l), wf);
+                unpack8(__ldg(reinterpret_cast<const uint4*>(w) + other), wo);
+            }
+            float x[8], y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 cs = trig[t][p0 + e];
-                        f[e] = l < hl ? f[e] * cs.x - o[e] * cs.y : f[e] * cs.x + o[e] * cs.y;
+            for (int e = 0; e < 8; ++e) {
+                const float2 cs = turned ? trig[warp][kHalf ? (low ? l : l - hl) * 8 + e : l * 4 + e / 2] : make_float2(1.0f, 0.0f);
+                x[e] = cs.x * wf[e];
+                y[e] = kHalf ? (low ? -cs.y : cs.y) * wo[e] : (e & 1 ? cs.y : -cs.y) * wf[e ^ 1];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) A[e] = pack_f32x2(x[2 * e], x[2 * e + 1]), B[e] = pack_f32x2(y[2 * e], y[2 * e + 1]);
+        }
+        for (int b = beg; b < end; b += R * kRows) {
+            uint4 cur[kRows];
+#pragma unroll
+            for (int n = 0; n < kRows; ++n) cur[n] = in[n];
+            const bool more = b + R * kRows < end;
+            load(more ? b + R * kRows : next, more ? end : next_end);
+            // every lane takes part in the shuffles: those past the end work on zeros and store nothing
+#pragma unroll
+            for (int n = 0; n < kRows; ++n) {
+                if (b + n * R >= end) break;
+                const int h = b + n * R + sub;
+                const bool live = h < end;
+                uint4 packed = cur[n];
+                float v[8];
+                unpack8(cur[n], v);
+                if constexpr (kKind != kValue) {
+                    uint64_t f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = pack_f32x2(v[2 * e], v[2 * e + 1]);
+                    uint64_t inv2 = pack_f32x2(1.0f, 1.0f);
+                    if (w) {
+                        uint64_t s2 = mul_f32x2(f[0], f[0]);
+#pragma unroll
+                        for (int e = 1; e < 4; ++e) s2 = fma_f32x2(f[e], f[e], s2);
+                        float s0, s1;
+                        unpack_f32x2(s2, s0, s1);
+                        const float inv = rsqrtf(group_sum<L>(s0 + s1) * (1.0f / D) + a.eps);
+                        inv2 = pack_f32x2(inv, inv);
+                    }
+                    uint64_t o[4];
+                    if constexpr (kHalf) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = pack_f32x2(__shfl_sync(0xFFFFFFFFu, v[2 * e], other, L),
+                                              __shfl_sync(0xFFFFFFFFu, v[2 * e + 1], other, L));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = pack_f32x2(v[2 * e + 1], v[2 * e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        unpack_f32x2(mul_f32x2(fma_f32x2(f[e], A[e], mul_f32x2(o[e], B[e])), inv2), v[2 * e], v[2 * e + 1]);
+                    packed = pack8(v);
+                }
+                if constexpr (kKind == kQuery) {
+                    if (live) reinterpret_cast<uint4*>(a.q_out + (tok * Hq + h) * D)[l] = packed;
+                } else {
+                    const int kh = h - (kKind == kKey ? Hq : Hq + Hk);
+                    if (kKind == kKey && live && a.k_out) reinterpret_cast<uint4*>(a.k_out + (tok * Hk + kh) * D)[l] = packed;
+                    if (row < 0) continue;
+                    const int64_t at = row + ((int64_t)kh << page_shift);
+                    void* cache = kKind == kKey ? a.cache.k : a.cache.v;
+                    if constexpr (kE4m3) {
+                        const float scale = row_scale(group_max<L>(top8(v)));
+                        if (live) {
+                            reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at * D)[l] = codes8(v, scale);
+                            if (l == 0) (kKind == kKey ? a.cache.ks : a.cache.vs)[at] = scale;
+                        }
+                    } else if (live) {
+                        reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + at * D)[l] = packed;
                     }
                 }
-            } else if (!is_v && l * 8 < a.rot_dim) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 cs = trig[t][l * 4 + e / 2];
-                    const float x = f[e], y = f[e + 1];
-                    f[e] = x * cs.x - y * cs.y;
-                    f[e + 1] = y * cs.x + x * cs.y;
-                }
             }
         }
-        const int kh = h < Hq ? 0 : (h - Hq) % Hk;
-        if (live && h < Hq) reinterpret_cast<uint4*>(a.q_out + (tok * Hq + h) * D)[l] = pack8(f);
-        if (live && h >= Hq && !is_v && a.k_out) reinterpret_cast<uint4*>(a.k_out + (tok * Hk + kh) * D)[l] = pack8(f);
-        if (!a.slots) continue;
-        const int slot = h >= Hq && live ? a.slots[tok] : -1;
-        const int page = slot / a.c.page_size;
-        const bool in = slot >= 0 && page < a.cache.num_pages;
-        if (slot >= 0 && !in && l == 0) set_error(a.err, MOE_ERR_BOUNDS);
-        const int64_t row = ((int64_t)page * Hk + kh) * a.c.page_size + slot % a.c.page_size;
-        if constexpr (kE4m3) {
-            if (!__any_sync(0xFFFFFFFFu, in)) continue;   // a warp may hold rows that are stored and others
-            const float scale = row_scale(group_max<L>(top8(f)));
-            if (in) {
-                reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) + row * D)[l] =
-                    codes8(f, scale);
-                if (l == 0) (is_v ? a.cache.vs : a.cache.ks)[row] = scale;
-            }
-        } else if (in) {
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? a.cache.v : a.cache.k) + row * D)[l] = pack8(f);
-        }
-    }
+    };
+    if (lo < q1) run(std::integral_constant<int, kQuery>{}, lo, q1, k0 < k1 ? k0 : v0, k0 < k1 ? k1 : v1);
+    if (k0 < k1) run(std::integral_constant<int, kKey>{}, k0, k1, v0, v1);
+    if (v0 < v1 && row >= 0) run(std::integral_constant<int, kValue>{}, v0, v1, 0, 0);
 }
 
 constexpr int kReadRows = 32;   // output rows per block
@@ -290,12 +358,16 @@ template <int D>
 cudaError_t prepare_dim(const AttnPrepareArgs& a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // one token a block while that leaves multiprocessors idle, then more, so that the angles are formed once for many rows
-    const int per = std::min(kTokMax, std::max(1, a.T / (8 * sms)));
-    const dim3 grid((a.T + per - 1) / per);
-    return a.c.cache_type == ATTN_CACHE_E4M3
-               ? launch_pdl(k_attn_prepare<D, true>, grid, dim3(kThreads), 0, st, a, per)
-               : launch_pdl(k_attn_prepare<D, false>, grid, dim3(kThreads), 0, st, a, per);
+    // a token's heads in as many parts as it takes to give each multiprocessor eight warps, one warp-wide load at least
+    const int H = a.c.q_heads + 2 * a.c.kv_heads, most = (H * (D / 8) + 31) / 32;
+    const int parts = std::max(1, std::min(most, 8 * sms / a.T));
+    int shift = 4;
+    while (1 << shift < a.c.page_size) ++shift;
+    const int64_t blocks = ((int64_t)a.T * parts + kPrepare / 32 - 1) / (kPrepare / 32);
+    auto kern = a.c.cache_type == ATTN_CACHE_E4M3
+                    ? (a.layout == ATTN_ROPE_HALF ? k_attn_prepare<D, true, true> : k_attn_prepare<D, true, false>)
+                    : (a.layout == ATTN_ROPE_HALF ? k_attn_prepare<D, false, true> : k_attn_prepare<D, false, false>);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kPrepare), 0, st, a, parts, shift);
 }
 
 template <int D>

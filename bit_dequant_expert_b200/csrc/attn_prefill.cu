@@ -48,10 +48,6 @@ constexpr int kN = 128;         // keys of a block
 constexpr int kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-#ifndef PF
-#define PF 450
-#endif
-constexpr int kPairsFrom = PF;   // blocks of two tiles from which pairs are taken
 constexpr float kGrow = 8.0f;   // log2 of the growth of a row's maximum that O is rescaled for
 
 enum Mode { kPairs, kHalves, kTurns };
@@ -636,8 +632,16 @@ cudaError_t prefill_mode(const AttnPrefillArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t prefill_dim(const AttnPrefillArgs& a, cudaStream_t st) {
-    if constexpr (D == 256) return prefill_mode<D, kTurns>(a, st);
-    else return most_items(a, 2) < kPairsFrom ? prefill_mode<D, kHalves>(a, st) : prefill_mode<D, kPairs>(a, st);
+    if constexpr (D == 256) {
+        return prefill_mode<D, kTurns>(a, st);
+    } else {
+        // Halves where pairs would leave the device half empty, or fill it hardly once with long rows of keys: the last
+        // tile then takes half as long.  B200, us (halves, pairs), 16 and 2 heads of 128: one prompt of 300 tokens 12, 15;
+        // 2048: 34, 45; 3000: 71, 78; 4096: 95, 81; four of 512: 22, 18; sixteen of 200: 40, 25.
+        const int64_t pairs = most_items(a, 2);
+        const bool halves = 2 * pairs <= 148 || (pairs < 200 && a.total_k >= (int64_t)1024 * a.B);
+        return halves ? prefill_mode<D, kHalves>(a, st) : prefill_mode<D, kPairs>(a, st);
+    }
 }
 
 }  // namespace
