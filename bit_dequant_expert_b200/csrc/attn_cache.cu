@@ -264,19 +264,23 @@ __global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareA
     if (v0 < v1 && row >= 0) run(std::integral_constant<int, kValue>{}, v0, v1, 0, 0);
 }
 
-constexpr int kReadRows = 32;   // output rows per block
+constexpr int kReadRows = 128;  // output rows per block at most
 constexpr int kReadUnroll = 4;  // loads a thread has in flight
 
 // Output rows in packed order: the sequence by a search over its boundaries,
-// once per row; then (k or v, row, head) units of L lanes.
+// once per row; then (row, head) units of D / 8 lanes, K's and then V's.
+// A lane steps from unit to unit by additions: divisions for its place
+// had the kernel bound by its instructions (65k rows of 2 heads of 128: 20.6
+// us).  Eight codes a lane, so that a warp's stores are whole lines (sixteen,
+// stored as two pieces 32 bytes apart: 24.4).
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a) {
-    constexpr int L = D / 8, kGroups = kThreads / L;
+__global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, int rows, int step_t, int step_h, int page_shift) {
+    constexpr int L = D / 8, kUnroll = kReadUnroll;
     __shared__ int64_t src[kReadRows];   // cache row of head 0, or -1: nothing to write, -2: zeros
     griddep_launch_dependents();
     griddep_wait();
-    const int r0 = blockIdx.x * kReadRows, Hk = a.c.kv_heads, P = a.c.page_size;
-    if (threadIdx.x < kReadRows) {
+    const int r0 = blockIdx.x * rows, Hk = a.c.kv_heads;
+    if (threadIdx.x < rows) {
         const int r = r0 + threadIdx.x;
         int64_t s = -1;
         if (r < a.total && r >= a.cu[0] && r < a.cu[a.B]) {
@@ -285,10 +289,10 @@ __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (a.cu[mid] <= r) lo = mid; else hi = mid - 1;
             }
-            const int j = r - a.cu[lo], p = j / P;
+            const int j = r - a.cu[lo], p = j >> page_shift;
             const int page = j >= 0 && p < a.table_stride ? a.page_table[lo * a.table_stride + p] : -1;
             if (page >= 0 && page < a.cache.num_pages) {
-                s = (int64_t)page * Hk * P + j % P;
+                s = ((int64_t)page * Hk << page_shift) + (j & ((1 << page_shift) - 1));
             } else {
                 s = -2;
                 set_error(a.err, MOE_ERR_BOUNDS);
@@ -298,52 +302,59 @@ __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a) {
     }
     if (blockIdx.x == 0 && threadIdx.x == 0 && (a.cu[a.B] > a.total || a.cu[0] < 0)) set_error(a.err, MOE_ERR_BOUNDS);
     __syncthreads();
+    using Piece = std::conditional_t<kE4m3, uint2, uint4>;
     const int l = threadIdx.x % L, g = threadIdx.x / L;
-    const int units = kReadRows * Hk;   // of k, then as many of v
-    for (int base = 0; base < 2 * units; base += kGroups * kReadUnroll) {
-        uint4 w[kReadUnroll];
-        uint2 c[kReadUnroll];
-        float scale[kReadUnroll];
-        int64_t row[kReadUnroll];
-        int64_t dst[kReadUnroll];
-        bool is_v[kReadUnroll];
+    const int first_t = g / Hk, first_h = g - first_t * Hk;
+    int t = first_t, h = first_h;
+    bool is_v = false;                       // K's units, then V's
+    while (!is_v || t < rows) {
+        if (t >= rows) is_v = true, t = first_t, h = first_h;
+        const Piece* cache = reinterpret_cast<const Piece*>(is_v ? a.cache.v : a.cache.k);
+        const float* scales = is_v ? a.cache.vs : a.cache.ks;
+        uint4* out = reinterpret_cast<uint4*>(is_v ? a.v_out : a.k_out);
+        Piece w[kUnroll];
+        float scale[kUnroll];
+        int64_t dst[kUnroll];                // in 16-byte pieces; -1: nothing to write
 #pragma unroll
-        for (int n = 0; n < kReadUnroll; ++n) {
-            const int u = base + n * kGroups + g;
-            is_v[n] = u >= units;
-            const int q = is_v[n] ? u - units : u;
-            const int t = q / Hk, h = q - t * Hk;
-            row[n] = u < 2 * units ? src[t] : -1;
-            dst[n] = ((int64_t)(r0 + t) * Hk + h) * D;
-            if (row[n] >= 0) {
-                row[n] += (int64_t)h * P;
-                const void* cache = is_v[n] ? a.cache.v : a.cache.k;
-                if constexpr (kE4m3) {
-                    c[n] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + row[n] * D) + l);
-                    scale[n] = __ldg((is_v[n] ? a.cache.vs : a.cache.ks) + row[n]);
-                } else {
-                    w[n] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + row[n] * D) + l);
-                }
-            } else {
-                c[n] = make_uint2(0u, 0u);
-                w[n] = make_uint4(0u, 0u, 0u, 0u);
-                scale[n] = 0.0f;
+        for (int n = 0; n < kUnroll; ++n) {
+            const int64_t row = t < rows ? src[t] : -1;
+            dst[n] = row == -1 ? -1 : ((int64_t)(r0 + t) * Hk + h) * L + l;
+            w[n] = Piece{};
+            scale[n] = 0.0f;
+            if (row >= 0) {
+                const int64_t at = row + ((int64_t)h << page_shift);
+                w[n] = __ldg(cache + at * L + l);
+                if (kE4m3) scale[n] = __ldg(scales + at);
             }
+            t += step_t, h += step_h;
+            if (h >= Hk) h -= Hk, ++t;
         }
 #pragma unroll
-        for (int n = 0; n < kReadUnroll; ++n) {
-            if (row[n] == -1) continue;
+        for (int n = 0; n < kUnroll; ++n) {
+            if (dst[n] < 0) continue;
             if constexpr (kE4m3) {
-                const uint32_t p0 = e4m3x2_to_f16x2(c[n].x & 0xFFFFu), p1 = e4m3x2_to_f16x2(c[n].x >> 16);
-                const uint32_t p2 = e4m3x2_to_f16x2(c[n].y & 0xFFFFu), p3 = e4m3x2_to_f16x2(c[n].y >> 16);
-                const float f[8] = {f16_lo(p0) * scale[n], f16_hi(p0) * scale[n], f16_lo(p1) * scale[n],
-                                    f16_hi(p1) * scale[n], f16_lo(p2) * scale[n], f16_hi(p2) * scale[n],
-                                    f16_lo(p3) * scale[n], f16_hi(p3) * scale[n]};
-                w[n] = pack8(f);
+                const uint64_t s2 = pack_f32x2(scale[n], scale[n]);
+                const uint32_t c[4] = {w[n].x & 0xFFFFu, w[n].x >> 16, w[n].y & 0xFFFFu, w[n].y >> 16};
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t p = e4m3x2_to_f16x2(c[e]);
+                    float lo, hi;
+                    unpack_f32x2(mul_f32x2(pack_f32x2(f16_lo(p), f16_hi(p)), s2), lo, hi);
+                    y[e] = pack_bf16x2(lo, hi);
+                }
+                out[dst[n]] = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+                out[dst[n]] = w[n];
             }
-            reinterpret_cast<uint4*>((is_v[n] ? a.v_out : a.k_out) + dst[n])[l] = w[n];
         }
     }
+}
+
+int page_shift_of(const attn_config_t& c) {
+    int shift = 4;
+    while (1 << shift < c.page_size) ++shift;
+    return shift;
 }
 
 int sm_count() {
@@ -361,20 +372,22 @@ cudaError_t prepare_dim(const AttnPrepareArgs& a, cudaStream_t st) {
     // a token's heads in as many parts as it takes to give each multiprocessor eight warps, one warp-wide load at least
     const int H = a.c.q_heads + 2 * a.c.kv_heads, most = (H * (D / 8) + 31) / 32;
     const int parts = std::max(1, std::min(most, 8 * sms / a.T));
-    int shift = 4;
-    while (1 << shift < a.c.page_size) ++shift;
     const int64_t blocks = ((int64_t)a.T * parts + kPrepare / 32 - 1) / (kPrepare / 32);
     auto kern = a.c.cache_type == ATTN_CACHE_E4M3
                     ? (a.layout == ATTN_ROPE_HALF ? k_attn_prepare<D, true, true> : k_attn_prepare<D, true, false>)
                     : (a.layout == ATTN_ROPE_HALF ? k_attn_prepare<D, false, true> : k_attn_prepare<D, false, false>);
-    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kPrepare), 0, st, a, parts, shift);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kPrepare), 0, st, a, parts, page_shift_of(a.c));
 }
 
 template <int D>
 cudaError_t read_dim(const AttnReadArgs& a, cudaStream_t st) {
-    const dim3 grid((a.total + kReadRows - 1) / kReadRows);
-    return a.c.cache_type == ATTN_CACHE_E4M3 ? launch_pdl(k_attn_read<D, true>, grid, dim3(kThreads), 0, st, a)
-                                             : launch_pdl(k_attn_read<D, false>, grid, dim3(kThreads), 0, st, a);
+    const bool e4m3 = a.c.cache_type == ATTN_CACHE_E4M3;
+    const int groups = kThreads / (D / 8);
+    // a row's sequence is searched once a block: many rows a block where there are enough for every multiprocessor
+    const int rows = std::min(kReadRows, std::max(8, a.total / (4 * std::max(1, sm_count()))));
+    const dim3 grid((a.total + rows - 1) / rows);
+    return launch_pdl(e4m3 ? k_attn_read<D, true> : k_attn_read<D, false>, grid, dim3(kThreads), 0, st, a, rows,
+                      groups / a.c.kv_heads, groups % a.c.kv_heads, page_shift_of(a.c));
 }
 
 }  // namespace
