@@ -4,7 +4,10 @@
 Argument marshalling only: every step of the layer runs in the CUDA library.
 The functions carry the C ABI's names (``include/moe_b200.h``); tensors are
 passed as torch tensors (their ``data_ptr()``), raw integer addresses or
-None (NULL).  ``stream`` defaults to torch's current CUDA stream.
+None (NULL).  ``stream`` defaults to torch's current CUDA stream.  The
+attention operators (``include/attn_b200.h``) go through a small extension
+module, ``_attn_binding``, which also checks their tensors' device, type and
+layout.
 
 Importing fails loudly when the library has not been built; there is no
 fallback implementation.
@@ -24,6 +27,8 @@ if not os.path.exists(LIB_PATH):
                       "(there is no fallback implementation)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _attn_binding as _attn  # noqa: E402  (the attention calls, without ctypes' cost per argument)
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -80,8 +85,6 @@ def attn_config(q_heads=16, kv_heads=2, head_dim=128, page_size=64, cache_type=A
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
-_I64 = ctypes.c_int64
-_F32 = ctypes.c_float
 _CFG = ctypes.POINTER(moe_config_t)
 
 _lib.moe_workspace_size.restype = ctypes.c_size_t
@@ -103,18 +106,6 @@ _lib.moe_combine.restype = _I32
 _lib.moe_combine.argtypes = [_CFG, _I32, _I32, _P, _P, _P, _P, _P, _P]
 _lib.gdn_scan.restype = _I32
 _lib.gdn_scan.argtypes = [_I32] * 6 + [_P] * 5 + [ctypes.c_float, _P, _P, _P, _P]
-_ACFG = ctypes.POINTER(attn_config_t)
-_lib.attn_qkv_prepare.restype = _I32
-_lib.attn_qkv_prepare.argtypes = [_ACFG, _I32, _P, _I64, _P, _P, _F32, _P, _I32, _I32, _F32, _P, _P, _I32] + [_P] * 8
-_lib.attn_kv_read.restype = _I32
-_lib.attn_kv_read.argtypes = [_ACFG, _I32, _I32, _P, _I64, _P, _I32] + [_P] * 8
-_lib.attn_prefill.restype = _I32
-_lib.attn_prefill.argtypes = [_ACFG, _I32, _I32, _I32, _P, _P, _P, _I64, _P, _I64, _P, _I64, _F32, _I32] + [_P] * 4
-_lib.attn_decode_workspace_size.restype = ctypes.c_size_t
-_lib.attn_decode_workspace_size.argtypes = [_ACFG, _I32, _I32, _I32]
-_lib.attn_decode.restype = _I32
-_lib.attn_decode.argtypes = [_ACFG, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _I32, _P, _P, _P, _P, _F32, _P, _P, _P,
-                             ctypes.c_size_t, _P, _P]
 _lib.moe_gather_rows.restype = _I32
 _lib.moe_gather_rows.argtypes = [_CFG, _I32, _P, _P, _P, _I32, _I32, _P, _P, _P, ctypes.c_size_t, _P]
 _lib.moe_get_device_error.restype = _I32
@@ -152,27 +143,10 @@ def _nbytes(t) -> int:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return _current_stream(_current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
-
-
-def _current_device() -> int:
-    return torch.cuda.current_device()
-
-
-def _current_stream(device: int) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-# torch's own direct reads of the current device and stream, several microseconds shorter than the calls above
-if hasattr(torch._C, "_cuda_getDevice") and hasattr(torch._C, "_cuda_getCurrentRawStream"):
-    def _current_device() -> int:   # noqa: F811
-        torch.cuda._lazy_init()
-        return torch._C._cuda_getDevice()
-
-    _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(status: int, call: str, raise_on_error: bool) -> int:
@@ -259,91 +233,42 @@ def gdn_scan(B, T, Hk, Hv, dk, dv, q, k, v, g, beta, scale, state_in, state_out,
     return _check(st, "gdn_scan", raise_on_error)
 
 
-def _bad_tensor(t, name: str, kind) -> None:
-    if not t.is_cuda:
-        raise ValueError("%s is on %s, not on a GPU" % (name, t.device))
-    if t.dtype is not kind:
-        raise TypeError("%s must be %s, got %s" % (name, kind, t.dtype))
-    raise ValueError("%s must be contiguous" % name)
-
-
-def _dptr(t, name: str, kind) -> int | None:
-    """_ptr of a contiguous tensor of type `kind` on the GPU."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is not kind or not t.is_cuda or not t.is_contiguous():
-        _bad_tensor(t, name, kind)
-    return t.data_ptr()
-
-
-def _rptr(t, name: str, kind) -> int | None:
-    """_ptr of a tensor of type `kind` on the GPU whose rows (along the first dimension) are contiguous."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is not kind or not t.is_cuda or not (t.is_contiguous() or (t.numel() and t[0].is_contiguous())):
-        _bad_tensor(t, name, kind)
-    return t.data_ptr()
-
-
-_BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
-
-
-def _cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale) -> tuple:
-    kind = _BF16
-    if cfg.cache_type == ATTN_CACHE_E4M3:   # codes may come as bytes
-        kind = torch.uint8 if getattr(k_cache, "dtype", None) is torch.uint8 else torch.float8_e4m3fn
-    return (_dptr(k_cache, "k_cache", kind), _dptr(v_cache, "v_cache", kind), _dptr(k_scale, "k_scale", _FP32),
-            _dptr(v_scale, "v_scale", _FP32))
-
-
 def attn_qkv_prepare(cfg, T, qkv, qkv_stride, q_weight, k_weight, eps, inv_freq, rot_dim, rope_layout, rope_scale,
                      positions, slots, num_pages, k_cache, v_cache, k_scale, v_scale, q_out, k_out, err=None,
                      stream=None, raise_on_error=True) -> int:
     """Norm of queries and keys, rotation of their positions, cache write (include/attn_b200.h)."""
-    st = _lib.attn_qkv_prepare(ctypes.byref(cfg), T, _rptr(qkv, "qkv", _BF16), qkv_stride,
-                               _dptr(q_weight, "q_weight", _BF16), _dptr(k_weight, "k_weight", _BF16), eps,
-                               _dptr(inv_freq, "inv_freq", _FP32), rot_dim, rope_layout, rope_scale,
-                               _dptr(positions, "positions", _INT32), _dptr(slots, "slots", _INT32), num_pages,
-                               *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), _dptr(q_out, "q_out", _BF16),
-                               _dptr(k_out, "k_out", _BF16), _dptr(err, "err", _INT32), _stream(stream))
+    st = _attn.attn_qkv_prepare(cfg, T, qkv, qkv_stride, q_weight, k_weight, eps, inv_freq, rot_dim, rope_layout,
+                                rope_scale, positions, slots, num_pages, k_cache, v_cache, k_scale, v_scale, q_out,
+                                k_out, err, stream)
     return _check(st, "attn_qkv_prepare", raise_on_error)
 
 
 def attn_kv_read(cfg, B, total, page_table, page_table_stride, cu_lens, num_pages, k_cache, v_cache, k_scale, v_scale,
                  k_out, v_out, err=None, stream=None, raise_on_error=True) -> int:
     """The cache's rows of each sequence, packed, in bf16 (include/attn_b200.h)."""
-    st = _lib.attn_kv_read(ctypes.byref(cfg), B, total, _rptr(page_table, "page_table", _INT32),
-                           page_table_stride, _dptr(cu_lens, "cu_lens", _INT32), num_pages,
-                           *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), _dptr(k_out, "k_out", _BF16),
-                           _dptr(v_out, "v_out", _BF16), _dptr(err, "err", _INT32), _stream(stream))
+    st = _attn.attn_kv_read(cfg, B, total, page_table, page_table_stride, cu_lens, num_pages, k_cache, v_cache,
+                            k_scale, v_scale, k_out, v_out, err, stream)
     return _check(st, "attn_kv_read", raise_on_error)
 
 
 def attn_prefill(cfg, B, total_q, total_k, cu_q, cu_k, q, q_stride, k, k_stride, v, v_stride, scale, causal, out,
                  lse=None, err=None, stream=None, raise_on_error=True) -> int:
     """Attention over packed prompts (include/attn_b200.h)."""
-    st = _lib.attn_prefill(ctypes.byref(cfg), B, total_q, total_k, _dptr(cu_q, "cu_q", _INT32),
-                           _dptr(cu_k, "cu_k", _INT32), _rptr(q, "q", _BF16), q_stride, _rptr(k, "k", _BF16),
-                           k_stride, _rptr(v, "v", _BF16), v_stride, scale, int(causal), _dptr(out, "out", _BF16),
-                           _dptr(lse, "lse", _FP32), _dptr(err, "err", _INT32), _stream(stream))
+    st = _attn.attn_prefill(cfg, B, total_q, total_k, cu_q, cu_k, q, q_stride, k, k_stride, v, v_stride, scale, causal,
+                            out, lse, err, stream)
     return _check(st, "attn_prefill", raise_on_error)
 
 
 def attn_decode_workspace_size(cfg, B: int, nq: int, max_len: int) -> int:
-    return int(_lib.attn_decode_workspace_size(ctypes.byref(cfg), B, nq, max_len))
+    return _attn.attn_decode_workspace_size(cfg, B, nq, max_len)
 
 
 def attn_decode(cfg, B, nq, max_len, q, q_stride, page_table, page_table_stride, seq_lens, num_pages, k_cache, v_cache,
                 k_scale, v_scale, scale, out, lse, ws, ws_bytes=None, err=None, stream=None,
                 raise_on_error=True) -> int:
     """Attention of a few new tokens per sequence over the cache (include/attn_b200.h)."""
-    n = _nbytes(ws) if ws_bytes is None else ws_bytes
-    st = _lib.attn_decode(ctypes.byref(cfg), B, nq, max_len, _rptr(q, "q", _BF16), q_stride,
-                          _rptr(page_table, "page_table", _INT32), page_table_stride,
-                          _dptr(seq_lens, "seq_lens", _INT32), num_pages,
-                          *_cache_ptrs(cfg, k_cache, v_cache, k_scale, v_scale), scale, _dptr(out, "out", _BF16),
-                          _dptr(lse, "lse", _FP32), _dptr(ws, "ws", torch.uint8), n, _dptr(err, "err", _INT32),
-                          _stream(stream))
+    st = _attn.attn_decode(cfg, B, nq, max_len, q, q_stride, page_table, page_table_stride, seq_lens, num_pages,
+                           k_cache, v_cache, k_scale, v_scale, scale, out, lse, ws, ws_bytes, err, stream)
     return _check(st, "attn_decode", raise_on_error)
 
 

@@ -1,4 +1,5 @@
-"""Builds the CUDA library libmoe_b200.so in-tree for sm_100a.
+"""Builds the CUDA library libmoe_b200.so in-tree for sm_100a, and the Python
+binding of its attention operators (_attn_binding, against the installed torch).
 
     python bit_dequant_expert_b200/build.py [--force] [--jobs N] [--ptxas-verbose]
 
@@ -11,10 +12,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -22,6 +25,8 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libmoe_b200.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_attn_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -55,6 +60,28 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in sources() + _deps())
 
 
+def binding_stale() -> bool:
+    if not os.path.exists(BINDING):
+        return True
+    t = os.path.getmtime(BINDING)
+    return any(os.path.getmtime(p) > t for p in (BINDING_SRC, os.path.join(INCLUDE, "attn_b200.h")))
+
+
+def build_binding() -> None:
+    """The extension module: host code only, linked to the library beside it and to torch's own libraries."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    libs = os.path.join(torch_dir, "lib")
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.check_call(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
+         "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
+         "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+         "-L", HERE, "-l:libmoe_b200.so", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+         "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], env=_env())
+    os.replace(tmp, BINDING)
+
+
 def _env() -> dict:
     """nvcc's temporary files go to a folder inside the repository."""
     tmpdir = os.path.join(BUILD, "tmp")
@@ -70,9 +97,15 @@ def _compile(src: str, extra: list[str]) -> str:
 
 
 def build(force: bool = False, jobs: int | None = None, extra: list[str] | None = None) -> str:
-    if not force and not stale():
-        return OUT
     os.makedirs(BUILD, exist_ok=True)
+    if force or stale():
+        _build_library(jobs, extra)
+    if force or binding_stale():
+        build_binding()
+    return OUT
+
+
+def _build_library(jobs: int | None, extra: list[str] | None) -> None:
     extra = extra or []
     srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
@@ -82,7 +115,6 @@ def build(force: bool = False, jobs: int | None = None, extra: list[str] | None 
     subprocess.check_call([nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp] + objs,
                           env=_env())
     os.replace(tmp, OUT)
-    return OUT
 
 
 def main(argv=None):
