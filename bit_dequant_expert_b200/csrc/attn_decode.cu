@@ -112,8 +112,13 @@ struct Cut {
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
 __device__ __forceinline__ int clamp_len(int len, int max_len) { return len < 0 ? 0 : min(len, max_len); }
 
+// a / b, in 32 bits where a fits (a 64-bit division takes several times as long).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (unsigned long long)a >> 32 || (unsigned long long)b >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 // Runs: block i of n takes tiles [total i / n, total (i + 1) / n).
-__device__ __forceinline__ long long run_start(long long total, int i, int n) { return total * i / n; }
+__device__ __forceinline__ long long run_start(long long total, int i, int n) { return quotient(total * i, n); }
 __device__ __forceinline__ int runs_of(long long total, int blocks) {
     return (int)min((long long)blocks, max(1ll, total / kMinTiles));
 }
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     }
     const long long start = run_start(total, blockIdx.x, runs), end = run_start(total, blockIdx.x + 1, runs);
     {
-        const long long at = start / U;
+        const long long at = quotient(start, U);
         if (tid < a.B && at >= first_before && at < first_before + first_n) {
             sm.find = tid;
             sm.scan[16] = first_before;
@@ -262,14 +267,14 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     }
     int b = sm.find, len = clamp_len(a.lens[b], a.max_len), nt = tiles_of(len);
     const long long rem = start - sm.scan[16] * U;
-    int u = (int)(rem / nt), tile = (int)(rem % nt);
+    int u = (int)quotient(rem, nt), tile = (int)(rem - (long long)u * nt);
     int left = (int)(end - start), it = 0;                   // tiles of the run to go, and done
     if (tid == 0) {
         Cut c = {-1, 0, b, u};
         if (tile > 0) {                                      // the runs that hold the unit's first and last tile
             const long long s0 = start - tile;
-            c.first = (int)(((s0 + 1) * runs - 1) / total);
-            c.count = (int)(((s0 + nt) * runs - 1) / total) - c.first + 1;
+            c.first = (int)quotient((s0 + 1) * runs - 1, total);
+            c.count = (int)quotient((s0 + nt) * runs - 1, total) - c.first + 1;
             if (c.first != (int)blockIdx.x - 1) c.first = -1;
         }
         cuts[blockIdx.x] = c;

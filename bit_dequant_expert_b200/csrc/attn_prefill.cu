@@ -95,6 +95,14 @@ __host__ __device__ constexpr int items_of(int lq, int G, int tiles) {
 __device__ bool find_work(const AttnPrefillArgs& a, int item, int G, int tiles, int* sh, int& seq, int& local) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
+    if (a.B == 1) {
+        const int q0 = a.cu_q[0], q1 = a.cu_q[1], k0 = a.cu_k[0], k1 = a.cu_k[1];
+        const bool bad = q0 < 0 || q1 < q0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k;
+        if (bad && tid == 0 && blockIdx.x == 0) set_error(a.err, MOE_ERR_BOUNDS);
+        seq = 0;
+        local = item;
+        return !bad && item < items_of(q1 - q0, G, tiles);
+    }
     if (tid == 0) sh[22] = -1;
     int total = 0;
     for (int base = 0; base < a.B; base += kThreads) {
@@ -178,6 +186,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    if (tid == 0) {
+        prefetch_tensormap(&q_map);
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+        mbar_init(&sm.q_full, 1);
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&sm.slot_full[i], 1);
+            mbar_init(&sm.slot_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 8);
+            mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.m_full[i], 4);
+        }
+        sm.dead = 0;
+        fence_mbar_init();
+    }
     griddep_launch_dependents();
     griddep_wait();   // everything read below may come from the previous grid
     int seq, local;
@@ -204,21 +230,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int nb = max(w.nb[0], w.nb[1]);
 
-    if (tid == 0) {
-        mbar_init(&sm.q_full, 1);
-        for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&sm.slot_full[i], 1);
-            mbar_init(&sm.slot_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 8);
-            mbar_init(&sm.o_done[i], 1);
-            mbar_init(&sm.m_full[i], 4);
-        }
-        sm.dead = 0;
-        fence_mbar_init();
-    }
     if (warp == 16) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
@@ -233,11 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 17) {
             // ---------------------------------------------------------- loads
             if (lane == 0 && nb > 0) {
-                prefetch_tensormap(&q_map);
-                prefetch_tensormap(&k_map);
-                prefetch_tensormap(&v_map);
                 mbar_arrive_expect_tx(&sm.q_full, (w.live[0] + w.live[1]) * C::kQBytes);
-    #pragma unroll
+#pragma unroll
                 for (int s = 0; s < C::kTiles; ++s)
                     if (w.live[s]) tma_load_3d(sm.q[s], &q_map, 0, w.q0 + w.row[s], w.head[s] * (D / 64), &sm.q_full);
                 int n = 0;   // slots issued so far
