@@ -46,7 +46,9 @@ namespace {
 constexpr int kTile = 64;            // keys of a tile
 constexpr int kSms = 148;
 constexpr int kProducers = 2;        // loading warps
-constexpr int kMinTiles = 2;         // tiles of a run at least
+constexpr int kUnitCost = 4;         // of beginning and ending a head's pass, in tiles (0: 62 ragged sequences of 2 heads of 256, 8
+                                     // rows each, took 63 us; 2: 41; 4: 36; 6: 37)
+constexpr int kMinPlaces = 2;        // places of a run at least (some then hold no tile)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -100.0f;    // log2 of the least value scale the running maximum follows
@@ -108,7 +110,9 @@ struct Cut {
     int b, u;                        // sequence, head and pass
 };
 
-// Tiles of a sequence's unit; an empty one has a tile without keys, which writes its zeros.
+// Tiles of a sequence's unit (a pass over a head's keys); an empty one has a tile without keys, which writes its zeros.
+// In the list a unit has kUnitCost places before its tiles', which stand for what beginning and ending it takes: a run
+// of many short sequences would else be far longer work than its tiles say.
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }
 __device__ __forceinline__ int clamp_len(int len, int max_len) { return len < 0 ? 0 : min(len, max_len); }
 
@@ -117,10 +121,10 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return (unsigned long long)a >> 32 || (unsigned long long)b >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-// Runs: block i of n takes tiles [total i / n, total (i + 1) / n).
+// Runs: block i of n takes places [total i / n, total (i + 1) / n).
 __device__ __forceinline__ long long run_start(long long total, int i, int n) { return quotient(total * i, n); }
 __device__ __forceinline__ int runs_of(long long total, int blocks) {
-    return (int)min((long long)blocks, max(1ll, total / kMinTiles));
+    return (int)min((long long)blocks, max(1ll, total / kMinPlaces));
 }
 
 // Codes 0 and 1 (lo) or 2 and 3 (hi) of w as an f16 pair (exact).
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
         if (b < a.B) {
             const int len = a.lens[b];
             if ((len < 0 || len > a.max_len) && blockIdx.x == 0) set_error(a.err, MOE_ERR_BOUNDS);
-            n = tiles_of(clamp_len(len, a.max_len));
+            n = tiles_of(clamp_len(len, a.max_len)) + kUnitCost;
         }
         long long inc = n;
 #pragma unroll
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
         long long before0 = 0;
         for (int base = 0; a.B > kThreads && base < a.B; base += kThreads) {
             const int b = base + tid;
-            const int n = b < a.B ? tiles_of(clamp_len(a.lens[b], a.max_len)) : 0;
+            const int n = b < a.B ? tiles_of(clamp_len(a.lens[b], a.max_len)) + kUnitCost : 0;
             long long inc = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -267,8 +271,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     }
     int b = sm.find, len = clamp_len(a.lens[b], a.max_len), nt = tiles_of(len);
     const long long rem = start - sm.scan[16] * U;
-    int u = (int)quotient(rem, nt), tile = (int)(rem - (long long)u * nt);
-    int left = (int)(end - start), it = 0;                   // tiles of the run to go, and done
+    int u = (int)quotient(rem, nt + kUnitCost), tile = (int)(rem - (long long)u * (nt + kUnitCost)) - kUnitCost;
+    int left = (int)(end - start) + min(tile, 0), it = 0;    // places of the run to go, from a tile on; tiles done
+    tile = max(tile, 0);
     if (tid == 0) {
         Cut c = {-1, 0, b, u};
         if (tile > 0) {                                      // the runs that hold the unit's first and last tile
@@ -299,8 +304,9 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
             };
             auto advance = [&]() {                           // to the next tile of the run
                 ++it, --left;
-                if (++tile < nt || left <= 0) return;
-                tile = 0;
+                if (++tile < nt) return;
+                tile = 0, left -= kUnitCost;
+                if (left <= 0) return;
                 if (++u == U) {
                     u = 0, ++b;
                     len = clamp_len(a.lens[b], a.max_len);
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                     }
                 }
                 mbar_arrive(&sm.q_full[buf]);
-                left -= nt - tile, tile = 0;
+                left -= nt - tile + kUnitCost, tile = 0;
                 if (left > 0 && ++u == U) {
                     u = 0, ++b;
                     len = clamp_len(a.lens[b], a.max_len);
@@ -465,7 +471,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
         }
         const int sees_all = len - a.nq + 1;                 // keys below this are seen by every row
 
-        for (int t = (grp + C::kGroups - it % C::kGroups) % C::kGroups; t < cnt; t += C::kGroups) {
+        const int turn0 = (grp + C::kGroups - it % C::kGroups) % C::kGroups;   // the group's first tile here
+        for (int t = turn0; t < cnt; t += C::kGroups) {
             while (place >= C::kStages) place -= C::kStages, turn ^= 1;
             const int st = place;
             place += C::kGroups;
@@ -682,10 +689,10 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
             }
             sm.fin[row][0] = M, sm.fin[row][1] = L;
         }
-        // one group after the other adds its outputs
+        // one group after the other adds its outputs, those that had a tile
 #pragma unroll 1
-        for (int round = 0; round < C::kGroups; ++round) {
-            if (round == grp) {
+        for (int round = 0; round < min(cnt, C::kGroups); ++round) {
+            if (round == turn0) {
 #pragma unroll
                 for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
         }
         // ------------------------------------------------------ the rows' outputs, or their part of them
         const bool whole = cnt == nt;
-        const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);   // a run ends at most one head's start and begins at most one's end
+        const int slot = 2 * blockIdx.x + (tile == 0 ? 1 : 0);   // a run cuts one unit at most at each end
         for (int i = tid; i < rows * (D / 4); i += kConsumers) {
             const int r = i / (D / 4), c = i % (D / 4);
             const float4 v = *reinterpret_cast<const float4*>(&sm.acc[r][4 * c]);
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                 if (c == 0) reinterpret_cast<float2*>(a.ws + g.ml_at)[at] = make_float2(M, L);
             }
         }
-        left -= cnt, it += cnt, tile = 0;
+        left -= cnt + kUnitCost, it += cnt, tile = 0;
         if (left > 0 && ++u == U) {
             u = 0, ++b;
             len = clamp_len(a.lens[b], a.max_len);
@@ -845,8 +852,8 @@ DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     g.row_blocks = (g.rows + g.row_pad - 1) / g.row_pad;
     g.units = c.kv_heads * g.row_blocks;
     // one block a multiprocessor, no more than the longest lengths give work to
-    const int64_t most = (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile);
-    g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most / kMinTiles));
+    const int64_t most = (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile + kUnitCost);
+    g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most / kMinPlaces));
     g.out_at = (int64_t)align256((size_t)g.blocks * sizeof(Cut));
     g.ml_at = g.out_at + (int64_t)2 * g.blocks * g.row_pad * c.head_dim * (int64_t)sizeof(float);
     return g;
