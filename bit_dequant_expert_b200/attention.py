@@ -122,7 +122,8 @@ class AttentionLayer:
             if cached:
                 k = torch.empty(total_k, c.kv_heads, c.head_dim, dtype=torch.bfloat16, device=self.device)
                 v = torch.empty_like(k)
-                attn_kv_read(c, B, total_k, page_table, max(1, page_table.stride(0)), cu_k, self.num_pages,
+                pages = page_table.contiguous()
+                attn_kv_read(c, B, total_k, pages, max(1, pages.shape[1]), cu_k, self.num_pages,
                              self.k_cache, self.v_cache, self.k_scale, self.v_scale, k, v, err=self.err)
                 v_stride = c.kv_heads * c.head_dim
             else:

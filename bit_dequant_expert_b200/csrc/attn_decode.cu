@@ -874,7 +874,7 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
     cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, NT>, smem, done);
     if (ce != cudaSuccess) return ce;
     ce = launch_pdl(k_attn_decode<D, kE4m3, NT>, dim3(g.blocks), dim3(C::kThreads), (size_t)smem, st, km, vm, a, g);
-    if (ce != cudaSuccess || g.blocks == 1) return ce;
+    if (ce != cudaSuccess || g.blocks == 1 || a.max_len <= kTile) return ce;   // no head's pass is cut
     return launch_pdl(k_attn_combine<D>, dim3(g.blocks - 1, 16), dim3(256), 0, st, a, g);
 }
 

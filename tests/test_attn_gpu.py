@@ -101,6 +101,7 @@ def check_prepared(c, d, T, rot, layout, got):
     (50, 3, 3, 128, 0, 0, True, 64, {}),
     (2500, 16, 2, 128, 128, 1, True, 64, dict(first=65536)),
     (1300, 32, 8, 64, 32, 0, False, 32, dict(skip=True)),
+    (40, 16, 2, 128, 96, 1, True, 16, dict(first=-70)),      # positions below zero too
 ])
 def test_prepare(T, hq, hkv, dim, rot, layout, e4m3, page, kw):
     c = m.attn_config(hq, hkv, dim, page, int(e4m3))
@@ -584,3 +585,99 @@ def test_layer_refusals():
     with pytest.raises(m.MoeError, match="MOE_ERR_BOUNDS"):
         L.check()
     L.check()
+
+
+# ------------------------------------------------------------------ the binding, streams
+
+
+def test_binding_refuses_tensors_too_small_for_the_call():
+    """What the library would read or write past a tensor's end is refused, as
+    are other types and layouts."""
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    i = lambda *s: z(*s, dt=torch.int32)  # noqa: E731
+    f = lambda *s: z(*s, dt=torch.float32)  # noqa: E731
+    c = m.attn_config(4, 2, 64, 16, m.ATTN_CACHE_E4M3)
+    kc = z(3, 2, 16, 64, dt=torch.uint8)
+
+    def prepare(**kw):
+        a = dict(T=4, qkv=z(4, 512), qkv_stride=512, q_weight=z(64), k_weight=z(64), eps=1e-6, inv_freq=f(32),
+                 rot_dim=64, rope_layout=0, rope_scale=1.0, positions=i(4), slots=i(4) - 1, num_pages=3, k_cache=kc,
+                 v_cache=kc, k_scale=f(3, 2, 16), v_scale=f(3, 2, 16), q_out=z(4, 4, 64), k_out=z(4, 2, 64))
+        a.update(kw)
+        return m.attn_qkv_prepare(c, *a.values())
+
+    def decode(**kw):
+        a = dict(B=2, nq=1, max_len=32, q=z(2, 4, 64), q_stride=256, page_table=i(2, 2), page_table_stride=2,
+                 seq_lens=i(2), num_pages=3, k_cache=kc, v_cache=kc, k_scale=f(3, 2, 16), v_scale=f(3, 2, 16),
+                 scale=0.1, out=z(2, 4, 64), lse=f(2, 4),
+                 ws=z(m.attn_decode_workspace_size(c, 2, 1, 32), dt=torch.uint8))
+        a.update(kw)
+        return m.attn_decode(c, *a.values())
+
+    def prefill(**kw):
+        a = dict(B=1, total_q=4, total_k=6, cu_q=i(2), cu_k=i(2), q=z(4, 4, 64), q_stride=256, k=z(6, 2, 64),
+                 k_stride=128, v=z(6, 2, 64), v_stride=128, scale=0.1, causal=True, out=z(4, 4, 64), lse=f(4, 4))
+        a.update(kw)
+        return m.attn_prefill(c, *a.values())
+
+    def read(**kw):
+        a = dict(B=2, total=5, page_table=i(2, 2), page_table_stride=2, cu_lens=i(3), num_pages=3, k_cache=kc,
+                 v_cache=kc, k_scale=f(3, 2, 16), v_scale=f(3, 2, 16), k_out=z(5, 2, 64), v_out=z(5, 2, 64))
+        a.update(kw)
+        return m.attn_kv_read(c, *a.values())
+
+    for call, bad in ((prepare, dict(qkv=z(3, 512))), (prepare, dict(qkv_stride=520)), (prepare, dict(q_weight=z(32))),
+                      (prepare, dict(inv_freq=f(16))), (prepare, dict(positions=i(3))), (prepare, dict(slots=i(3))),
+                      (prepare, dict(num_pages=4)), (prepare, dict(k_scale=f(3, 2, 8))), (prepare, dict(q_out=z(3, 4, 64))),
+                      (prepare, dict(k_out=z(3, 2, 64))), (decode, dict(q=z(1, 4, 64))), (decode, dict(seq_lens=i(1))),
+                      (decode, dict(page_table=i(1, 2))), (decode, dict(num_pages=5)), (decode, dict(out=z(1, 4, 64))),
+                      (decode, dict(lse=f(4))), (prefill, dict(q=z(3, 4, 64))), (prefill, dict(k=z(5, 2, 64))),
+                      (prefill, dict(v_stride=136)), (prefill, dict(cu_q=i(1))), (prefill, dict(out=z(3, 4, 64))),
+                      (prefill, dict(lse=f(15))), (read, dict(total=6)), (read, dict(page_table=i(2, 1))),
+                      (read, dict(cu_lens=i(2))), (read, dict(v_out=z(4, 2, 64)))):
+        with pytest.raises(ValueError, match="may touch"):
+            call(**bad)
+    with pytest.raises(m.MoeError, match="WORKSPACE"):
+        decode(ws=z(128, dt=torch.uint8))
+    with pytest.raises(TypeError, match="qkv must be"):
+        prepare(qkv=f(4, 512))
+    with pytest.raises(TypeError, match="seq_lens must be"):
+        decode(seq_lens=i(2).long())
+    with pytest.raises(ValueError, match="out must be contiguous"):
+        prefill(out=z(4, 64, 4).transpose(1, 2))
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        prefill(q=z(4, 64, 4).transpose(1, 2))
+    assert prepare() == 0 and decode() == 0 and prefill() == 0 and read() == 0
+    torch.cuda.synchronize()
+
+
+def test_calls_follow_their_stream():
+    """On a stream other than torch's current one, given or current, the calls
+    come after the work before them there."""
+    g = rng(31)
+    table, pages = R.make_table(g, [300, 77], 16)
+    kc, vc, ks, vs = R.make_cache(g, pages, 2, 16, 128, True)
+    c = m.attn_config(8, 2, 128, 16, 1)
+    q = torch.randn(2, 8, 128, generator=g).bfloat16()
+    lens = torch.tensor([300, 77], dtype=torch.int32)
+    kd, vd, ksd, vsd, tb, ln, q0 = R.cuda(kc, vc, ks, vs, table, lens, q)
+    ws = [torch.empty(m.attn_decode_workspace_size(c, 2, 1, 300), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    qd = [torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    outs = [torch.empty(2, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    big = torch.zeros(64 << 20, device="cuda")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for n, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            big.add_(1.0)              # keeps the stream busy before the queries arrive
+            qd[n].copy_(q0)
+            args = (c, 2, 1, 300, qd[n], 1024, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, 0.1, outs[n], None, ws[n])
+            if n:
+                m.attn_decode(*args)
+        if not n:
+            m.attn_decode(*args, stream=s)
+    torch.cuda.synchronize()
+    for b, n in enumerate((300, 77)):
+        ref = R.attend(q[b:b + 1], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), 0.1, [n])
+        for out in outs:
+            R.check_attention(out[b:b + 1].cpu(), None, ref)
