@@ -70,7 +70,7 @@ struct Smem {
     uint8_t slot[C::kSlots][C::kSlot];
     float m[2][kM], top[2][kM];                               // a group's maxima, handed on; between a row's threads
     uint64_t q_full, slot_full[C::kSlots], slot_empty[C::kSlots];
-    uint64_t s_full[2], p_full[2], o_done[2], m_full[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_done[2], m_full[2];   // p_half: the first 32 of each 64 keys
     uint32_t tmem_base;
     int dead;                                                 // a bounded wait expired: every role leaves
     int find[24];                                             // scan of the work list; the block's item
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_half[i], 8);
             mbar_init(&sm.p_full[i], 8);
             mbar_init(&sm.o_done[i], 1);
             mbar_init(&sm.m_full[i], 4);
@@ -319,8 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_commit_warp(issue, &sm.s_full[buf]);
                 };
-                // O `s` += P V, P in bf16 over the S buffer: each half of the keys over its own scores
-                auto product_o = [&](int s, int buf, int first, bool add) {
+                // O `s` += P V, P in bf16 over the S buffer: each half of the keys over its own scores.  The softmax
+                // threads hand P over in two parts, the first 32 and the last 32 keys of each half.
+                auto product_o = [&](int s, int buf, int first, bool add, uint32_t parity) {
                     constexpr int kKeys = kN / C::kParts;
                     const uint32_t d = tmem + C::kOCol + s * D, pa = tmem + buf * kN;
                     uint32_t vb[C::kParts];
@@ -328,9 +330,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int p = 0; p < C::kParts; ++p)   // the next 64 columns lie a panel of kKeys rows on
                         vb[p] = slot_lo + (first + p) % C::kSlots * (C::kSlot / 16) + smem_desc_lo(0, kKeys * 128);
 #pragma unroll
-                    for (int kk = 0; kk < kN / 16; ++kk)
-                        tc_mma_ts_warp(issue, d, pa + kk / 4 * 64 + kk % 4 * 8, vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi,
-                                       kIdO, add || kk != 0);
+                    for (int part = 0; part < 2; ++part) {
+                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_live(part ? &sm.p_full[buf] : &sm.p_half[buf], parity,
+                                                                          &sm.dead, a.err));
+                        tc_fence_after();
+                        if (!ok) return;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int kk = (i & 1) + (i >> 1) * 4 + part * 2;
+                            tc_mma_ts_warp(issue, d, pa + kk / 4 * 64 + kk % 4 * 8,
+                                           vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi, kIdO,
+                                           add || part + i != 0);
+                        }
+                    }
                     tc_commit_warp(issue, &sm.o_done[s]);
                 };
                 // values past the last key any row of the block sees are zeroed: they may hold NaN, and 0 NaN is NaN
@@ -369,11 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         bool have = false;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            if (j < (s ? nb1 : nb0) && ok) {
-                                ok = __all_sync(0xFFFFFFFFu, mbar_wait_live(&sm.p_full[s], j & 1, &sm.dead, a.err));
-                                tc_fence_after();
-                                if (ok) product_o(s, s, vf, j > 0);
-                            }
+                            if (j < (s ? nb1 : nb0) && ok) product_o(s, s, vf, j > 0, j & 1);
                             if (j + 1 < (s ? nb1 : nb0) && ok) {
                                 if (!have) kf = take();
                                 have = true;
@@ -396,10 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < nb && ok; ++j) {
                         const int vf = take(), g = j & 1;
                         if (j == nb - 1 && ok) zero_tail(vf);
-                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_live(&sm.p_full[g], (j >> 1) & 1, &sm.dead, a.err));
-                        tc_fence_after();
+                        if (ok) product_o(kMode == kHalves ? g : 0, g, vf, kMode == kHalves ? j > 1 : j > 0, (j >> 1) & 1);
                         if (!ok) break;
-                        product_o(kMode == kHalves ? g : 0, g, vf, kMode == kHalves ? j > 1 : j > 0);
                         release(vf);
                         if (j + 2 < nb) {
                             kf = take();
@@ -519,6 +525,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p[i] = pack_bf16x2(lo, hi);
                 }
                 tmem_st16(p_addr + 16 * h, p);
+                if (h == 0) {                                   // the product begins on these
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_half[grp]);
+                }
             }
             {
                 float lo, hi;
