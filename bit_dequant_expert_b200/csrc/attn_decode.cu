@@ -178,8 +178,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     using C = Cfg<D, kE4m3, NT>;
     constexpr int kThreads = C::kThreads, kConsumers = C::kConsumers;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem<D, kE4m3, NT>& sm =
-        *reinterpret_cast<Smem<D, kE4m3, NT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<D, kE4m3, NT>& sm = *reinterpret_cast<Smem<D, kE4m3, NT>*>(align1024(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hk = a.c.kv_heads, Hq = a.c.q_heads, G = Hq / Hk, ps = g.page_shift;
     const int ss = min(ps, 6), sub = 1 << ss;        // rows of a TMA box
@@ -540,7 +539,6 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                     lv[h] = fmaxf(lg2(vs[h]), kLeast);
                 }
             }
-            bool grow = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -550,11 +548,25 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         x[h] = NT == 1 ? s[r][2 * h + e] + s2[r][2 * h + e] : s[r][2 * h + e];
                         x[h] *= ks[h] * qs[r][e];
-                        if (masked && key0 + gr + 8 * h >= lim[r][e]) x[h] = -CUDART_INF_F;
                         s[r][2 * h + e] = x[h];
                     }
-                    grow = grow || (kE4m3 ? fmaxf(x[0] + lv[0], x[1] + lv[1]) : fmaxf(x[0], x[1])) > m[r][e] + kGrow;
                 }
+            if (masked) {
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (key0 + gr + 8 * (x >> 1) >= lim[r][x & 1]) s[r][x] = -CUDART_INF_F;
+            }
+            float over = -CUDART_INF_F;                      // the most by which a score passes its row's maximum
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = kE4m3 ? fmaxf(s[r][e] + lv[0], s[r][2 + e] + lv[1]) : fmaxf(s[r][e], s[r][2 + e]);
+                    over = x > m[r][e] ? fmaxf(over, x - m[r][e]) : over;
+                }
+            const bool grow = over > kGrow;
             // ---- running maximum: exchanged only where some score of the group has grown past it.  This barrier also
             // says that the group is done with the probabilities of its tile before, and the next with these zeros
             if (named_barrier_or(2 + grp, 128, grow || !ok)) {

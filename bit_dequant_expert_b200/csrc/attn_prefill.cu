@@ -177,12 +177,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap v_map, const AttnPrefillArgs a) {
     using C = Cfg<D, kMode>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    Smem<D, kMode>& sm = *reinterpret_cast<Smem<D, kMode>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem<D, kMode>& sm = *reinterpret_cast<Smem<D, kMode>*>(align1024(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Hk = a.c.kv_heads, G = a.c.q_heads / Hk;
     const int kvh = blockIdx.x % Hk;
     if (reinterpret_cast<uint8_t*>(&sm + 1) > smem_raw + dynamic_smem_bytes()) {   // dynamic memory begins off its 1024 bytes
-        set_error(a.err, MOE_ERR_TIMEOUT);
+        set_error(a.err, MOE_ERR_UNSUPPORTED);
         return;
     }
 

@@ -12,6 +12,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// The next multiple of 1024 bytes of the shared window at or after p (which
+// stays a shared-memory pointer to the compiler: through an integer it would
+// lose that, and every access become a generic one).
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) { return p + (-smem_u32(p) & 1023u); }
+
 __device__ __forceinline__ uint32_t dynamic_smem_bytes() {
     uint32_t n;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(n));
