@@ -72,7 +72,9 @@ struct Cfg {
     static constexpr int kRest =
         kRows * (D * 4 + (D + kPad) * 4 + 8 * 4 * kGroups + 4 * kGroups + 16) + kGroups * NT * 1024 + 1024;
     static constexpr int kFit = (226 * 1024 - kRest) / (kStage + kTile * 8 + 16);
-    static constexpr int kStages = kFit > 12 ? 12 : kFit;
+    // a stage is filled by one warp and taken by one group, which so wait for its phases one after another: a barrier's
+    // parity does not tell a phase from the one two before it
+    static constexpr int kStages = (kFit > 12 ? 12 : kFit) / kGroups * kGroups;
     static constexpr bool kQRegs = NT == 1 && D <= 128;       // query fragments in registers
 };
 
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
 
     if (tid >= kConsumers) {
         const int pw = warp - kConsumers / 32;
-        // ------------------------------------------------------ loads: two warps take alternate tiles
+        // ------------------------------------------------------ loads: two warps take alternate stages
         if (pw < kProducers) {
             // lanes 0-15 serve K, 16-31 V: of four keys each, the scales (one 16-byte copy) and, where a page's box
             // begins, the box
@@ -314,7 +316,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                 }
                 kvh = u / g.row_blocks;
             };
-            for (int i = 0; i < pw; ++i) advance();
+            auto mine = [&]() { return it % C::kStages % kProducers == pw; };
+            while (left > 0 && !mine()) advance();
             bool ok = true;
             int page = left > 0 ? page_at() : -2;
             while (left > 0) {
@@ -322,7 +325,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                 const bool in = page != -2, good = in && page >= 0 && page < a.cache.num_pages;
                 if (in && !good) set_error(a.err, MOE_ERR_BOUNDS);
                 const int row = good ? ((page * Hk + kvh) << ps) + ((tile * kTile + quad) & ((1 << ps) - 1)) : pad_row;
-                for (int i = 0; i < kProducers; ++i) advance();
+                do advance();
+                while (left > 0 && !mine());
                 if (left > 0) page = page_at();              // on its way while this tile waits for its place
                 if (use > 0) {
                     ok = mbar_wait_live(&sm.empty[st], (use - 1) & 1, &sm.dead, a.err);
@@ -882,7 +886,7 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
         return cudaErrorInvalidValue;
     static int done[64] = {0};
     const int smem = (int)sizeof(Smem<D, kE4m3, NT>) + 1024;
-    static_assert(sizeof(Smem<D, kE4m3, NT>) + 1024 <= 232448 && C::kStages >= 2, "shared memory per block");
+    static_assert(sizeof(Smem<D, kE4m3, NT>) + 1024 <= 232448 && C::kStages >= C::kGroups, "shared memory per block");
     cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, NT>, smem, done);
     if (ce != cudaSuccess) return ce;
     ce = launch_pdl(k_attn_decode<D, kE4m3, NT>, dim3(g.blocks), dim3(C::kThreads), (size_t)smem, st, km, vm, a, g);

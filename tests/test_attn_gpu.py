@@ -408,6 +408,45 @@ def test_decode_many_sequences(e4m3):
     run_decode(lens[200:], 3, 16, 2, 128, e4m3, 32, 16)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 2, 4, 8])
+def test_decode_long_runs_from_cold_memory(nq, dim, e4m3):
+    """Runs of many tiles whose loads arrive at uneven times (a cold cache,
+    pages in any order, some of them shared): each call gives the same bits,
+    and what the definition says."""
+    hq, hkv, page, pages = 16, 2, 64, 1500
+    g = torch.Generator(device="cuda").manual_seed(nq + dim)
+    lens = [int(n) for n in torch.randint(1, 8193, (40,), generator=rng(nq))] + [100, 1500]
+    kc, vc = (torch.randn(pages, hkv, page, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    ks = vs = None
+    if e4m3:
+        (kc, ks), (vc, vs) = R.quantised(kc.float()), R.quantised(vc.float())
+    table = torch.randint(0, pages, (len(lens), 128), generator=g, device="cuda", dtype=torch.int32)
+    q = (torch.randn(len(lens) * nq, hq, dim, generator=g, device="cuda") * 1.5).bfloat16()
+    c, top = m.attn_config(hq, hkv, dim, page, int(e4m3)), max(lens)
+    ws = torch.empty(m.attn_decode_workspace_size(c, len(lens), nq, top), dtype=torch.uint8, device="cuda")
+    ln, err, cold = torch.tensor(lens, dtype=torch.int32, device="cuda"), err_word(), torch.zeros(64 << 20, device="cuda")
+    first = None
+    for _ in range(6):
+        cold.sum()                                       # 256 MB: more than the cache holds
+        out = torch.full((len(lens) * nq, hq, dim), math.nan, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((len(lens) * nq, hq), math.nan, device="cuda")
+        assert m.attn_decode(c, len(lens), nq, top, q, hq * dim, table, table.stride(0), ln, pages, kc, vc, ks, vs,
+                             dim ** -0.5, out, lse, ws, err=err) == 0
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    for b in (len(lens) - 2, len(lens) - 1):
+        used = table[b, :(lens[b] + page - 1) // page].long()
+        rows = [R.rows_of(x[used].cpu(), None if s is None else s[used].cpu(), torch.arange(len(used)), lens[b])
+                for x, s in ((kc, ks), (vc, vs))]
+        r = slice(b * nq, b * nq + nq)
+        ref = R.attend(q[r].cpu(), *rows, dim ** -0.5, [lens[b] - nq + i + 1 for i in range(nq)])
+        R.check_attention(first[0][r].cpu(), first[1][r].cpu(), ref)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A bad page reads as zeros (score 0, value 0) and is reported; so is a
     length above max_len (cut) or below zero (none)."""
