@@ -63,6 +63,12 @@ struct Cfg {
     static constexpr int kGroups = D * NT <= 256 ? 3 : 2;
     static constexpr int kConsumers = 128 * kGroups;
     static constexpr int kThreads = kConsumers + 128;
+    // registers a thread: what the block is launched with, and, where a consumer's work does not fit that, what loaders
+    // and consumers then have (64 rows of 128 elements, 250k keys of two heads in 8 bits: 144 us with 168 registers, 96 with 224)
+    static constexpr bool kSplitRegs = D * NT > 512 || NT == 8;
+    static constexpr int kRegs = 65536 / kThreads / 8 * 8, kRegsLoad = 56;
+    static constexpr int kRegsWork = (kRegs * kThreads - 128 * kRegsLoad) / kConsumers / 8 * 8;
+    static_assert(!kSplitRegs || kRegsWork * kConsumers + kRegsLoad * 128 <= kRegs * kThreads, "registers of the block");
     static constexpr int kCols = D / 64;                     // tiles of 16 columns of the output a warp has
     static constexpr int kRow = D * (kE4m3 ? 1 : 2);         // bytes of a cache row
     static constexpr int kBlock = kRow < 128 ? kRow : 128;   // swizzled bytes of a row's blocks
@@ -287,6 +293,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     }
 
     if (tid >= kConsumers) {
+        if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsLoad));
         const int pw = warp - kConsumers / 32;
         // ------------------------------------------------------ loads: two warps take alternate stages
         if (pw < kProducers) {
@@ -426,6 +433,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     // lanes 0-7 and 8-15 the pair of pieces, 16-31 the other 8 keys
     constexpr int kMask = C::kBlock == 128 ? 7 : 3, kShift = C::kBlock == 128 ? 0 : 1;
     constexpr int kPieces = C::kBlock / 16;                  // 16-byte pieces of a block
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsWork));
     constexpr bool kTwoKeys = kE4m3 && C::kCols == 1;
     const uint32_t block_bytes = sub * C::kBlock;            // from one block of a row to the next
     auto key_at = [&](int key) {                             // a multiple of 16 within the tile: 16 keys lie in one box
@@ -889,6 +897,10 @@ cudaError_t decode_launch(const AttnDecodeArgs& a, const DecodeGrid& g, cudaStre
     static_assert(sizeof(Smem<D, kE4m3, NT>) + 1024 <= 232448 && C::kStages >= C::kGroups, "shared memory per block");
     cudaError_t ce = set_smem_once(k_attn_decode<D, kE4m3, NT>, smem, done);
     if (ce != cudaSuccess) return ce;
+    if (C::kSplitRegs) {                                     // the consumers would wait for registers that are not there
+        static const bool there = has_registers(k_attn_decode<D, kE4m3, NT>, C::kRegs);
+        if (!there) return cudaErrorInvalidConfiguration;
+    }
     ce = launch_pdl(k_attn_decode<D, kE4m3, NT>, dim3(g.blocks), dim3(C::kThreads), (size_t)smem, st, km, vm, a, g);
     if (ce != cudaSuccess || g.blocks == 1 || a.max_len <= kTile) return ce;   // no head's pass is cut
     return launch_pdl(k_attn_combine<D>, dim3(g.blocks - 1, 16), dim3(256), 0, st, a, g);

@@ -645,6 +645,9 @@ cudaError_t prefill_mode(const AttnPrefillArgs& a, cudaStream_t st) {
     static_assert(sizeof(Smem<D, kMode>) <= 232448, "shared memory per block");
     cudaError_t ce = set_smem_once(k_attn_prefill<D, kMode>, smem, done);
     if (ce != cudaSuccess) return ce;
+    constexpr int kRegs = (kRegsSoftmax * 512 + kRegsOther * 128) / kThreads;   // else the warps would wait for them
+    static const bool there = has_registers(k_attn_prefill<D, kMode>, kRegs);
+    if (!there) return cudaErrorInvalidConfiguration;
     const int64_t blocks = most_items(a, C::kTiles);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     return launch_pdl(k_attn_prefill<D, kMode>, dim3((unsigned)blocks), dim3(kThreads), (size_t)smem, st, qm, km, vm, a);

@@ -90,6 +90,14 @@ inline cudaError_t set_smem_once(Kern* k, int bytes, int* set_bytes) {
     return ce;
 }
 
+// Whether a kernel was given at least n registers a thread: what a block hands
+// from some of its warps to others (setmaxnreg) must come with its launch.
+template <typename Kern>
+inline bool has_registers(Kern* k, int n) {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, k) == cudaSuccess && at.numRegs >= n;
+}
+
 // Launch with programmatic dependent launch allowed: the kernel may start
 // while the previous grid on the stream finishes, and must execute
 // griddepcontrol.wait before touching anything that grid writes or reads.
