@@ -373,38 +373,51 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                 // the halves of k)
                 constexpr int kLanes = D / 16, kAtOnce = 32 / kLanes;
                 const int c = lane % kLanes;
-#pragma unroll 2
-                for (int r0 = (pw - kProducers) * kAtOnce; r0 < C::kRows; r0 += (4 - kProducers) * kAtOnce) {
-                    const int r = r0 + lane / kLanes;
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-                    if (r < rows) {
-                        const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
-                        const uint4* src =
-                            reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
-                        x = src[2 * c];
-                        y = src[2 * c + 1];
-                    }
-                    if constexpr (kE4m3) {
-                        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                        uint32_t top = 0u;                   // largest exponent of the row (bits 7..14 of an element)
+                // (four steps' loads are on their way together, as the first head's products wait for them: 32 rows of 128
+                // elements took 54 us with two, 52 with four; two where the registers went to the consumers)
+                constexpr int kStep = (4 - kProducers) * kAtOnce, kAll = (C::kRows + kStep - 1) / kStep;
+                constexpr int kMost = C::kSplitRegs ? 2 : 4, kMany = kAll < kMost ? kAll : kMost;
+#pragma unroll 1
+                for (int r0 = (pw - kProducers) * kAtOnce; r0 < C::kRows; r0 += kMany * kStep) {
+                    uint4 xs[kMany], ys[kMany];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7F80u, (w[i] >> 16) & 0x7F80u));
-#pragma unroll
-                        for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                        top >>= 7;
-                        // 2^(127 - top); a row of zeros, or with an infinity or NaN, stays as it is
-                        const int e = top == 255u || top == 0u ? 127 : min(max(254 - (int)top, 1), 254);
-                        const float up = __int_as_float(e << 23);
-                        if (c == 0 && r < C::kRows) sm.q_scale[buf][r] = __int_as_float(max(254 - e, 1) << 23);
-                        x = make_uint4(bf16x2_to_f16x2(w[0], up), bf16x2_to_f16x2(w[2], up), bf16x2_to_f16x2(w[4], up),
-                                       bf16x2_to_f16x2(w[6], up));
-                        y = make_uint4(bf16x2_to_f16x2(w[1], up), bf16x2_to_f16x2(w[3], up), bf16x2_to_f16x2(w[5], up),
-                                       bf16x2_to_f16x2(w[7], up));
+                    for (int i = 0; i < kMany; ++i) {
+                        const int r = r0 + i * kStep + lane / kLanes;
+                        xs[i] = ys[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < rows) {
+                            const int q = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
+                            const uint4* src =
+                                reinterpret_cast<const uint4*>(a.q + (int64_t)(b * a.nq + q) * a.q_stride + (int64_t)h * D);
+                            xs[i] = src[2 * c];
+                            ys[i] = src[2 * c + 1];
+                        }
                     }
-                    if (r < C::kRows) {
-                        uint8_t* dst = sm.q[buf] + r * (D * 2);
-                        *reinterpret_cast<uint4*>(dst + ((2 * c) ^ (r & 7)) * 16) = x;
-                        *reinterpret_cast<uint4*>(dst + ((2 * c + 1) ^ (r & 7)) * 16) = y;
+#pragma unroll
+                    for (int i = 0; i < kMany; ++i) {
+                        const int r = r0 + i * kStep + lane / kLanes;
+                        uint4 x = xs[i], y = ys[i];
+                        if constexpr (kE4m3) {
+                            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                            uint32_t top = 0u;               // largest exponent of the row (bits 7..14 of an element)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = max(top, max(w[e] & 0x7F80u, (w[e] >> 16) & 0x7F80u));
+#pragma unroll
+                            for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                            top >>= 7;
+                            // 2^(127 - top); a row of zeros, or with an infinity or NaN, stays as it is
+                            const int e = top == 255u || top == 0u ? 127 : min(max(254 - (int)top, 1), 254);
+                            const float up = __int_as_float(e << 23);
+                            if (c == 0 && r < C::kRows) sm.q_scale[buf][r] = __int_as_float(max(254 - e, 1) << 23);
+                            x = make_uint4(bf16x2_to_f16x2(w[0], up), bf16x2_to_f16x2(w[2], up), bf16x2_to_f16x2(w[4], up),
+                                           bf16x2_to_f16x2(w[6], up));
+                            y = make_uint4(bf16x2_to_f16x2(w[1], up), bf16x2_to_f16x2(w[3], up), bf16x2_to_f16x2(w[5], up),
+                                           bf16x2_to_f16x2(w[7], up));
+                        }
+                        if (r < C::kRows) {
+                            uint8_t* dst = sm.q[buf] + r * (D * 2);
+                            *reinterpret_cast<uint4*>(dst + ((2 * c) ^ (r & 7)) * 16) = x;
+                            *reinterpret_cast<uint4*>(dst + ((2 * c + 1) ^ (r & 7)) * 16) = y;
+                        }
                     }
                 }
                 mbar_arrive(&sm.q_full[buf]);
