@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                     const float* p = &sm.scale[st][16 * w + gr + 8 * h];
                     ks[h] = p[0] * sc;
                     vs[h] = key0 + gr + 8 * h < len ? p[kTile] : 0.0f;   // scales past the end may be anything
-                    lv[h] = fmaxf(lg2(vs[h]), kLeast);
+                    lv[h] = fmaxf(lg2(fabsf(vs[h])), kLeast);
                 }
             }
 #pragma unroll
