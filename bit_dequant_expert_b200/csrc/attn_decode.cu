@@ -13,7 +13,7 @@
 // probabilities go to its group through shared memory, and it adds all 64
 // keys' values to a quarter of the output's columns, so that outputs take few
 // registers and no key is converted twice.  A group keeps the running maximum
-// m of each row, exchanged only when some score exceeds it by 2^8.  Where the
+// m of each row, exchanged only when some probability passes 2^15.  Where the
 // run leaves a sequence's head, the groups are joined in shared memory.  A
 // head that one block did whole is finished there; of one cut at a run's end
 // (O, m, l) go to the workspace for k_attn_combine.
@@ -25,10 +25,12 @@
 // rows 0-7, the odd ones as 8-15.  A query row is brought to a largest magnitude in
 // [1, 2) by a power of two (exact: bf16 has fewer bits; what falls below
 // 2^-24 of the row's largest is under the sums' own rounding), a key's scale
-// multiplies its score, a value's its probability.  The running maximum m is
-// that of score + log2 of the value's scale, so that a probability times its
-// scale, p = exp2(s - m) vs, stays at most 2^8 and the largest near 1: it is
-// rounded to f16, 2^-11 of itself or 2^-25 of the largest.
+// multiplies its score, a value's its probability.  The running maximum m
+// follows that of score + log2 of the value's scale, 7 below it, so that a
+// probability times its scale, p = exp2(s - m) vs, stays at most 2^15 and the
+// largest at 2^7 or more: it is rounded to f16, 2^-12 of itself or 2^-32 of the
+// largest.  (The largest may be that of a row of zeros, whose scale is 1 by
+// the cache's definition beside much smaller ones: the 7 bits are theirs.)
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -51,8 +53,9 @@ constexpr int kUnitCost = 4;         // of beginning and ending a head's pass, i
 constexpr int kMinPlaces = 2;        // places of a run at least (some then hold no tile)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLeast = -100.0f;    // log2 of the least value scale the running maximum follows
-constexpr float kGrow = 8.0f;        // log2 of the growth of a row's maximum that O is rescaled for
+constexpr float kLead = 7.0f;        // log2 of a row's largest probability (times its value's scale) when m is set
+constexpr float kGrow = 15.0f;       // and of what it may grow to before O is rescaled: below the largest f16
+constexpr float kLeast = -80.0f;     // log2 of the least value scale that m follows: 2^31 probabilities of 2^95 stay finite
 
 // Tiles of 8 query rows that a block works on at once (more rows take more passes over the keys).
 int row_tiles(int rows, int dim) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 || dim == 256 ? 4 : 8; }
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                     for (int x = 0; x < 4; ++x)
                         if (key0 + gr + 8 * (x >> 1) >= lim[r][x & 1]) s[r][x] = -CUDART_INF_F;
             }
-            float over = -CUDART_INF_F;                      // the most by which a score passes its row's maximum
+            float over = -CUDART_INF_F;                      // the most by which a score passes its row's m
 #pragma unroll
             for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -617,8 +620,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                         const float x = fmaxf(fmaxf(sm.top[grp][0][row], sm.top[grp][1][row]),
                                               fmaxf(sm.top[grp][2][row], sm.top[grp][3][row]));
                         if (x > m[r][e] + kGrow) {
-                            const float f = ex2(m[r][e] - x);
-                            m[r][e] = x;
+                            const float n = x - kLead, f = ex2(m[r][e] - n);
+                            m[r][e] = n;
                             l[r][e] *= f;
 #pragma unroll
                             for (int i = 0; i < C::kCols; ++i) o[r][i][e] *= f, o[r][i][2 + e] *= f;

@@ -447,6 +447,35 @@ def test_decode_long_runs_from_cold_memory(nq, dim, e4m3):
         R.check_attention(first[0][r].cpu(), first[1][r].cpu(), ref)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 4])
+def test_decode_small_values_beside_rows_of_zeros(nq, dim):
+    """A row of zeros has the scale 1, the rows beside it 2.4 2^-24: their
+    probabilities keep their bits (half a step of 2^-32 of the largest: 0.07%
+    here, within the 2^-8 that check_attention allows a probability)."""
+    g, page, lens, hkv = rng(nq), 64, [600, 77], 2
+    table, pages = R.make_table(g, lens, page)
+    kc, ks = R.quantised(torch.randn(pages, hkv, page, dim, generator=g))
+    v = torch.randn(dim, generator=g)
+    v = (v * (448 * 2.4 * 2.0 ** -24 / v.abs().max())).expand(pages, hkv, page, dim).clone()
+    v[:, :, 1::2] = 0.0
+    vc, vs = R.quantised(v)
+    assert (vs[:, :, 1::2] == 1.0).all()
+    q = torch.zeros(len(lens) * nq, 16, dim, dtype=torch.bfloat16)    # every key counts alike
+    c, top = m.attn_config(16, hkv, dim, page, m.ATTN_CACHE_E4M3), max(lens)
+    ws = torch.empty(m.attn_decode_workspace_size(c, len(lens), nq, top), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    qd, tb, ln, kd, vd, ksd, vsd = R.cuda(q, table, torch.tensor(lens, dtype=torch.int32), kc, vc, ks, vs)
+    m.attn_decode(c, len(lens), nq, top, qd, 16 * dim, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, dim ** -0.5, out,
+                  lse, ws)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        r = slice(b * nq, b * nq + nq)
+        ref = R.attend(q[r], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), dim ** -0.5,
+                       [n - nq + i + 1 for i in range(nq)])
+        R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A bad page reads as zeros (score 0, value 0) and is reported; so is a
     length above max_len (cut) or below zero (none)."""
