@@ -81,6 +81,8 @@ struct AttnDecodeArgs {
 cudaError_t launch_attn_prepare(const AttnPrepareArgs& a, cudaStream_t st);
 cudaError_t launch_attn_read(const AttnReadArgs& a, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnPrefillArgs& a, cudaStream_t st);
+// Whether a call's keys can be counted in 32 bits (a sequence's, and a block's tiles).
+bool attn_decode_counts(const attn_config_t& c, int B, int nq, int max_len);
 size_t attn_decode_ws_bytes(const attn_config_t& c, int B, int nq, int max_len);
 cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t st);
 

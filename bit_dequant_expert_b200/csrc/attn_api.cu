@@ -47,7 +47,9 @@ AttnCache cache_of(const attn_config_t* c, int32_t num_pages, const void* k, con
     return a;
 }
 
-bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (int64_t)1 << 31; }
+constexpr int64_t kMaxStride = (int64_t)1 << 31;   // elements; offsets of 2^31 rows then fit 64 bits
+
+bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= kMaxStride; }
 
 }  // namespace
 
@@ -102,7 +104,7 @@ int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const i
     moe::ApiRange api_range("attn_kv_read");
     int32_t st = check_config(cfg);
     if (st) return st;
-    if (B < 1 || total < 0 || page_table_stride < 1) return MOE_ERR_INVALID_ARG;
+    if (B < 1 || total < 0 || page_table_stride < 1 || page_table_stride > kMaxStride) return MOE_ERR_INVALID_ARG;
     if (total == 0) return MOE_OK;
     if (!page_table || !cu_lens || !k_out || !v_out || !aligned(page_table, 4) || !aligned(cu_lens, 4) ||
         !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(err, 4))
@@ -163,6 +165,7 @@ int32_t attn_prefill(const attn_config_t* cfg, int32_t B, int32_t total_q, int32
 
 size_t attn_decode_workspace_size(const attn_config_t* cfg, int32_t B, int32_t nq, int32_t max_len) {
     if (check_config(cfg) || B < 1 || B > 65535 || nq < 1 || nq > 8 || max_len < 1) return 0;
+    if (!attn_decode_counts(*cfg, B, nq, max_len)) return 0;
     return attn_decode_ws_bytes(*cfg, B, nq, max_len);
 }
 
@@ -178,7 +181,9 @@ int32_t attn_decode(const attn_config_t* cfg, int32_t B, int32_t nq, int32_t max
         return MOE_ERR_INVALID_ARG;
     if (B > 65535 || nq > 8) return MOE_ERR_UNSUPPORTED;
     if (!row_stride_ok(q_stride, (int64_t)cfg->q_heads * cfg->head_dim)) return MOE_ERR_INVALID_ARG;
-    if (page_table_stride < (max_len + (int64_t)cfg->page_size - 1) / cfg->page_size) return MOE_ERR_INVALID_ARG;
+    if (page_table_stride < (max_len + (int64_t)cfg->page_size - 1) / cfg->page_size || page_table_stride > kMaxStride)
+        return MOE_ERR_INVALID_ARG;
+    if (!attn_decode_counts(*cfg, B, nq, max_len)) return MOE_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(err, 4))
         return MOE_ERR_INVALID_ARG;

@@ -883,6 +883,11 @@ __global__ void __launch_bounds__(256) k_attn_combine(const AttnDecodeArgs a, co
     }
 }
 
+// Places in the list of all runs, were each sequence max_len long.
+int64_t most_places(const DecodeGrid& g, int B, int max_len) {
+    return (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile + kUnitCost);
+}
+
 DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     DecodeGrid g;
     g.page_shift = 4;
@@ -892,8 +897,7 @@ DecodeGrid decode_grid(const attn_config_t& c, int B, int nq, int max_len) {
     g.row_blocks = (g.rows + g.row_pad - 1) / g.row_pad;
     g.units = c.kv_heads * g.row_blocks;
     // one block a multiprocessor, no more than the longest lengths give work to
-    const int64_t most = (int64_t)B * g.units * ((max_len + (int64_t)kTile - 1) / kTile + kUnitCost);
-    g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most / kMinPlaces));
+    g.blocks = (int)std::min<int64_t>(kSms, std::max<int64_t>(1, most_places(g, B, max_len) / kMinPlaces));
     g.out_at = (int64_t)align256((size_t)g.blocks * sizeof(Cut));
     g.ml_at = g.out_at + (int64_t)2 * g.blocks * g.row_pad * c.head_dim * (int64_t)sizeof(float);
     return g;
@@ -941,6 +945,10 @@ cudaError_t decode_dim(const AttnDecodeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+bool attn_decode_counts(const attn_config_t& c, int B, int nq, int max_len) {
+    return max_len <= 1 << 30 && most_places(decode_grid(c, B, nq, max_len), B, max_len) / kSms < 0x7FFFFF00;
+}
 
 size_t attn_decode_ws_bytes(const attn_config_t& c, int B, int nq, int max_len) {
     const DecodeGrid g = decode_grid(c, B, nq, max_len);

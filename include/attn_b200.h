@@ -29,7 +29,7 @@
  *    uint16_t bits.  Every array of bf16, codes or scales and the workspace
  *    is 16-byte aligned, 32-bit index and fp32 arrays 4-byte aligned, except
  *    where a call says more.
- *  - Row strides count elements and are multiples of 8; a row holds its heads
+ *  - Row strides count elements and are multiples of 8, up to 2^31; a row holds its heads
  *    one after another, [heads, head_dim].  Outputs are contiguous.
  *  - Paged cache: k_cache and v_cache [num_pages, kv_heads, page_size,
  *    head_dim]; slot s is row s % page_size of page s / page_size.
@@ -39,6 +39,8 @@
  *    page_size]: the value is code * scale, scale = max|row| / 448 (1 for a
  *    row of zeros), the code rounded to nearest even.  A row with a
  *    non-finite element gets a NaN scale: all of it reads as NaN.
+ *    (attn_decode: beside a row of zeros, values below 2^-12 lose bits,
+ *    as their scales fall below 2^-21 of its.)
  *  - `err` (may be NULL): a device word for what only the device can see; the
  *    first error of any call stays in it until the caller clears it, and the
  *    kernel carries on with safe values.  MOE_ERR_BOUNDS: a slot, page or
@@ -114,9 +116,9 @@ int32_t attn_qkv_prepare(const attn_config_t* cfg, int32_t T, const uint16_t* qk
  *              outside [cu_lens[0], cu_lens[B]) are left as they are; rows
  *              past total are not written and reported (MOE_ERR_BOUNDS).
  *   page_table int32 rows of page indices, page_table_stride elements apart
- *              (>= 1; any value, not only multiples of 8).  A page outside
- *              [0, num_pages) or past the row's end is reported and reads as
- *              zeros.
+ *              (1 .. 2^31; any value, not only multiples of 8), all of which
+ *              a row holds.  A page outside [0, num_pages) or past the row's
+ *              end is reported and reads as zeros.
  *   k_out, v_out  bf16 [total, kv_heads, head_dim].
  */
 int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const int32_t* page_table,
@@ -125,7 +127,7 @@ int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const i
                      uint16_t* v_out, int32_t* err, void* stream);
 
 /*
- * Attention of B >= 1 packed sequences.  Sequence b has query rows
+ * Attention of B (1..65535) packed sequences.  Sequence b has query rows
  * cu_q[b] .. cu_q[b + 1] - 1 and key/value rows cu_k[b] .. cu_k[b + 1] - 1
  * (either may be empty).  causal: the last query sees every key of its
  * sequence, the one before it all but the last, and so on (queries of a
@@ -153,7 +155,9 @@ int32_t attn_prefill(const attn_config_t* cfg, int32_t B, int32_t total_q, int32
  * the cache.  Sequence b has seq_lens[b] rows in the cache, the new tokens'
  * among them; its token i (query row b nq + i) sees rows
  * 0 .. seq_lens[b] - nq + i (none: zeros, lse -inf).
- *   max_len    >= 1: no sequence is longer (a longer one is reported and
+ *   max_len    1 .. 2^30 (else, or where B, the heads and max_len together
+ *              pass 2^44 keys or so, MOE_ERR_UNSUPPORTED, and a workspace size
+ *              of 0): no sequence is longer (a longer one is reported and
  *              cut).  page_table rows hold at least ceil(max_len / page_size)
  *              entries; a page outside [0, num_pages) is reported and reads
  *              as zeros.

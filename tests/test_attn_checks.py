@@ -110,6 +110,17 @@ def test_decode_refuses(bad, status):
     assert decode(**bad) == status
 
 
+def test_counts_and_strides_past_the_limits_are_refused():
+    far = (1 << 31) + 8
+    assert read(page_table_stride=far) == INV and decode(page_table_stride=far) == INV
+    assert decode(max_len=(1 << 30) + 1, page_table_stride=1 << 25) == UNS
+    assert decode(B=65535, max_len=1 << 30, page_table_stride=1 << 25) == UNS
+    c = cfg()
+    assert m.attn_decode_workspace_size(c, 1, 1, 1 << 30) > 0
+    assert m.attn_decode_workspace_size(c, 1, 1, (1 << 30) + 1) == 0
+    assert m.attn_decode_workspace_size(c, 65535, 1, 1 << 30) == 0
+
+
 def test_workspace_size():
     c = cfg()
     assert m.attn_decode_workspace_size(c, 1, 1, 1) > 0
