@@ -265,14 +265,15 @@ __global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareA
 }
 
 constexpr int kReadRows = 128;  // output rows per block at most
-constexpr int kReadUnroll = 4;  // loads a thread has in flight
+constexpr int kReadUnroll = 2;  // units a thread has in flight, K's and V's of each
 
 // Output rows in packed order: the sequence by a search over its boundaries,
-// once per row; then (row, head) units of D / 8 lanes, K's and then V's.
-// A lane steps from unit to unit by additions: divisions for its place
-// had the kernel bound by its instructions (65k rows of 2 heads of 128: 20.6
-// us).  Eight codes a lane, so that a warp's stores are whole lines (sixteen,
-// stored as two pieces 32 bytes apart: 24.4).
+// once per row; then (row, head) units of D / 8 lanes.  Places are worked out
+// once for K and V, which lie alike, and a lane steps from unit to unit by
+// additions, as the kernel is bound by its instructions next to its bytes
+// (65k rows of 2 heads of 128 in 8 bits, 100 MB: 16.5 us, 6.1 TB/s; K's units
+// and then V's: 19.8).  Eight codes a lane, so that a warp's stores are whole
+// lines.  Two units at once (four: 19.4).
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, int rows, int step_t, int step_h, int page_shift) {
     constexpr int L = D / 8, kUnroll = kReadUnroll;
@@ -304,27 +305,22 @@ __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, in
     __syncthreads();
     using Piece = std::conditional_t<kE4m3, uint2, uint4>;
     const int l = threadIdx.x % L, g = threadIdx.x / L;
-    const int first_t = g / Hk, first_h = g - first_t * Hk;
-    int t = first_t, h = first_h;
-    bool is_v = false;                       // K's units, then V's
-    while (!is_v || t < rows) {
-        if (t >= rows) is_v = true, t = first_t, h = first_h;
-        const Piece* cache = reinterpret_cast<const Piece*>(is_v ? a.cache.v : a.cache.k);
-        const float* scales = is_v ? a.cache.vs : a.cache.ks;
-        uint4* out = reinterpret_cast<uint4*>(is_v ? a.v_out : a.k_out);
-        Piece w[kUnroll];
-        float scale[kUnroll];
+    int t = g / Hk, h = g - t * Hk;
+    while (t < rows) {
+        Piece w[kUnroll][2];                 // K's and V's, which lie alike
+        float scale[kUnroll][2];
         int64_t dst[kUnroll];                // in 16-byte pieces; -1: nothing to write
 #pragma unroll
         for (int n = 0; n < kUnroll; ++n) {
             const int64_t row = t < rows ? src[t] : -1;
             dst[n] = row == -1 ? -1 : ((int64_t)(r0 + t) * Hk + h) * L + l;
-            w[n] = Piece{};
-            scale[n] = 0.0f;
+            w[n][0] = w[n][1] = Piece{};
+            scale[n][0] = scale[n][1] = 0.0f;
             if (row >= 0) {
                 const int64_t at = row + ((int64_t)h << page_shift);
-                w[n] = __ldg(cache + at * L + l);
-                if (kE4m3) scale[n] = __ldg(scales + at);
+                w[n][0] = __ldg(static_cast<const Piece*>(a.cache.k) + at * L + l);
+                w[n][1] = __ldg(static_cast<const Piece*>(a.cache.v) + at * L + l);
+                if (kE4m3) scale[n][0] = __ldg(a.cache.ks + at), scale[n][1] = __ldg(a.cache.vs + at);
             }
             t += step_t, h += step_h;
             if (h >= Hk) h -= Hk, ++t;
@@ -332,20 +328,24 @@ __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, in
 #pragma unroll
         for (int n = 0; n < kUnroll; ++n) {
             if (dst[n] < 0) continue;
-            if constexpr (kE4m3) {
-                const uint64_t s2 = pack_f32x2(scale[n], scale[n]);
-                const uint32_t c[4] = {w[n].x & 0xFFFFu, w[n].x >> 16, w[n].y & 0xFFFFu, w[n].y >> 16};
-                uint32_t y[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t p = e4m3x2_to_f16x2(c[e]);
-                    float lo, hi;
-                    unpack_f32x2(mul_f32x2(pack_f32x2(f16_lo(p), f16_hi(p)), s2), lo, hi);
-                    y[e] = pack_bf16x2(lo, hi);
+            for (int x = 0; x < 2; ++x) {
+                uint4* out = reinterpret_cast<uint4*>(x ? a.v_out : a.k_out) + dst[n];
+                if constexpr (kE4m3) {
+                    const uint64_t s2 = pack_f32x2(scale[n][x], scale[n][x]);
+                    const uint32_t c[4] = {w[n][x].x & 0xFFFFu, w[n][x].x >> 16, w[n][x].y & 0xFFFFu, w[n][x].y >> 16};
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t p = e4m3x2_to_f16x2(c[e]);
+                        float lo, hi;
+                        unpack_f32x2(mul_f32x2(pack_f32x2(f16_lo(p), f16_hi(p)), s2), lo, hi);
+                        y[e] = pack_bf16x2(lo, hi);
+                    }
+                    *out = make_uint4(y[0], y[1], y[2], y[3]);
+                } else {
+                    *out = w[n][x];
                 }
-                out[dst[n]] = make_uint4(y[0], y[1], y[2], y[3]);
-            } else {
-                out[dst[n]] = w[n];
             }
         }
     }

@@ -626,6 +626,45 @@ def test_layer_decode_captured_and_replayed():
     L.check()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_layer_prompt_captured_and_replayed(e4m3):
+    """A prompt's next chunk (write, read-back, attention) in a graph, replayed
+    on new rows and lengths of the same sums: what plain calls give."""
+    g, L, qw, kw, inv = layer_case(e4m3)
+    page = L.cfg.page_size
+    table = torch.randperm(L.num_pages, generator=g)[:20].view(2, 10).int().cuda()
+    T, total = 37, 300
+    qkv = torch.zeros(T, L.row, dtype=torch.bfloat16, device="cuda")
+    pos, sl = (torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2))
+    cu_q, cu_k = (torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2))
+
+    def fill(new, held):
+        p = torch.cat([torch.arange(k - n, k) for n, k in zip(new, held)])
+        b = torch.repeat_interleave(torch.arange(2), torch.tensor(new))
+        qkv.copy_(torch.randn(T, L.row, generator=g).bfloat16())
+        pos.copy_(p.int())
+        sl.copy_((table.cpu().long()[b, p // page] * page + p % page).int())
+        cu_q.copy_(torch.tensor([0, new[0], T], dtype=torch.int32))
+        cu_k.copy_(torch.tensor([0, held[0], total], dtype=torch.int32))
+
+    def call():
+        return L.prefill(qkv, pos, sl, cu_q, page_table=table, cu_k=cu_k, total_k=total)
+
+    fill((30, 7), (140, 160))
+    call()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = call()
+    for new, held in (((30, 7), (140, 160)), ((1, 36), (1, 299)), ((37, 0), (300, 0))):
+        fill(new, held)
+        gr.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.isfinite(got.float()).all() and torch.equal(got, call())
+    L.check()
+
+
 def test_layer_refusals():
     _, L, *_ = layer_case(False)
     z = lambda *s, **kw: torch.zeros(*s, **{**dict(dtype=torch.int32, device="cuda"), **kw})  # noqa: E731
