@@ -99,10 +99,27 @@ __device__ __forceinline__ float row_scale(float top) {
     return s > 0.0f ? s : 1.401298464e-45f;
 }
 
+// Codes of f / s.  One division a row: with r = 1 / s and q = f r, the quotient
+// is q + (f - q s) r, whose remainder one fused step gives exactly (Markstein's
+// correction); what is left before the last rounding is below 2^-46 of it.
+// (A division an element: 16384 tokens of 20 heads of 128 took 47 us.)
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float s) {
+    float q[8];
+    if (s >= 8.0779357e-28f && s <= 1.2379400e27f) {   // 2^-90 .. 2^90: nothing that becomes a code but 0 leaves the range
+        const float r = 1.0f / s;
+        const uint64_t r2 = pack_f32x2(r, r), s2 = pack_f32x2(-s, -s);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const uint64_t x = pack_f32x2(f[e], f[e + 1]), y = mul_f32x2(x, r2);
+            unpack_f32x2(fma_f32x2(fma_f32x2(y, s2, x), r2, y), q[e], q[e + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = f[e] / s;
+    }
     uint2 w;
-    w.x = pack_e4m3x2(f[0] / s, f[1] / s) | (uint32_t)pack_e4m3x2(f[2] / s, f[3] / s) << 16;
-    w.y = pack_e4m3x2(f[4] / s, f[5] / s) | (uint32_t)pack_e4m3x2(f[6] / s, f[7] / s) << 16;
+    w.x = pack_e4m3x2(q[0], q[1]) | (uint32_t)pack_e4m3x2(q[2], q[3]) << 16;
+    w.y = pack_e4m3x2(q[4], q[5]) | (uint32_t)pack_e4m3x2(q[6], q[7]) << 16;
     return w;
 }
 

@@ -144,6 +144,31 @@ def test_prepare_edge_rows_and_bad_slots():
 # ------------------------------------------------------------------ read
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prepare_codes_are_those_of_a_division(dim):
+    """Value rows of every size, ties among them: code for code what a 32-bit
+    division and one rounding to nearest even give."""
+    g, T, hkv, page = rng(dim), 4096, 2, 64
+    v = torch.randn(T, hkv, dim, generator=g)
+    v[::3] = torch.randint(-448, 449, v[::3].shape, generator=g).float() / 32   # quotients on and next to borders
+    v *= torch.exp2(torch.randint(-126, 121, (T, hkv, 1), generator=g).float())
+    v[5], v[7, :, 1:] = 0.0, 0.0
+    v = v.bfloat16()
+    qkv = torch.cat([torch.zeros(T, (1 + hkv) * hkv * dim, dtype=torch.bfloat16), v.flatten(1)], 1).cuda()
+    c = m.attn_config(hkv * hkv, hkv, dim, page, m.ATTN_CACHE_E4M3)
+    kc, vc = (torch.zeros(T // page, hkv, page, dim, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros(T // page, hkv, page, device="cuda") for _ in range(2))
+    q = torch.empty(T, hkv * hkv, dim, dtype=torch.bfloat16, device="cuda")
+    m.attn_qkv_prepare(c, T, qkv, qkv.stride(0), None, None, 0.0, None, 0, 0, 1.0, None,
+                       torch.arange(T, dtype=torch.int32, device="cuda"), T // page, kc, vc, ks, vs, q, None)
+    torch.cuda.synchronize()
+    codes, scales = (t.cpu().transpose(1, 2).flatten(0, 1) for t in (vc.view(torch.uint8), vs))
+    want, s = R.quantised(v.float())
+    normal = (s >= 2.0 ** -126) & torch.isfinite(s)      # scales that are numbers of full precision
+    assert normal.float().mean() > 0.9 and torch.equal(scales[normal], s[normal])
+    assert torch.equal(codes[normal], want.view(torch.uint8)[normal])
+
+
 @pytest.mark.parametrize("lens,hkv,dim,e4m3,page", [
     ([1], 2, 128, True, 64), ([0, 33, 0, 1, 128, 0], 1, 64, True, 16), ([257, 64, 63], 8, 256, False, 32),
     ([777], 2, 256, True, 128), ([5, 700, 31, 1], 3, 128, False, 64), (list(range(0, 40)), 2, 64, False, 16)])
