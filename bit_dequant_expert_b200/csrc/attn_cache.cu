@@ -59,14 +59,11 @@ __device__ __forceinline__ float group_sum(float v) {
     for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-// Largest of the group's values; NaN when any is NaN.
+// Largest of the group's values.
 template <int L>
-__device__ __forceinline__ float group_max(float v) {
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) {
-        const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        v = (u > v || u != u) ? u : v;
-    }
+    for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
 
@@ -79,14 +76,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// Largest magnitude of 8 elements; NaN when any is NaN.
-__device__ __forceinline__ float top8(const float (&f)[8]) {
-    float top = 0.0f;
+// Bits of the largest magnitude of 8 elements: as whole numbers they are in
+// the magnitudes' order, and a NaN's are above all.
+__device__ __forceinline__ uint32_t top8(const float (&f)[8]) {
+    uint32_t top = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(f[e]);
-        top = (m > top || m != m) ? m : top;
-    }
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
     return top;
 }
 
@@ -242,10 +237,14 @@ __global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareA
                     }
                     uint64_t o[4];
                     if constexpr (kHalf) {
+                        const uint4 w8 = make_uint4(__shfl_sync(0xFFFFFFFFu, cur[n].x, other, L),
+                                                    __shfl_sync(0xFFFFFFFFu, cur[n].y, other, L),
+                                                    __shfl_sync(0xFFFFFFFFu, cur[n].z, other, L),
+                                                    __shfl_sync(0xFFFFFFFFu, cur[n].w, other, L));
+                        float u[8];
+                        unpack8(w8, u);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = pack_f32x2(__shfl_sync(0xFFFFFFFFu, v[2 * e], other, L),
-                                              __shfl_sync(0xFFFFFFFFu, v[2 * e + 1], other, L));
+                        for (int e = 0; e < 4; ++e) o[e] = pack_f32x2(u[2 * e], u[2 * e + 1]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[e] = pack_f32x2(v[2 * e + 1], v[2 * e]);
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareA
                     const int64_t at = row + ((int64_t)kh << page_shift);
                     void* cache = kKind == kKey ? a.cache.k : a.cache.v;
                     if constexpr (kE4m3) {
-                        const float scale = row_scale(group_max<L>(top8(v)));
+                        const float scale = row_scale(__uint_as_float(group_max<L>(top8(v))));
                         if (live) {
                             reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at * D)[l] = codes8(v, scale);
                             if (l == 0) (kKind == kKey ? a.cache.ks : a.cache.vs)[at] = scale;
