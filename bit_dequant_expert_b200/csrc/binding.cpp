@@ -6,8 +6,9 @@
 // A pointer argument is a tensor, a raw integer address or None (NULL).  A
 // tensor must be on the current CUDA device, of the type the call reads,
 // contiguous (where the call takes a row stride: contiguous within each index
-// of its first dimension) and hold all that the call may touch.  The stream is an integer, an object with a
-// cuda_stream attribute, or None: torch's current stream.
+// of its first dimension) and hold all that the call may touch.  The stream is
+// an integer, an object with a cuda_stream attribute, or None: torch's current
+// stream.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -26,6 +27,7 @@ struct Fail {};   // a Python exception is set
 struct Args {
     PyObject* const* a;
     Py_ssize_t n, i = 0;
+    int device = -1;   // the current one, once a tensor is to be compared with it
 
     Args(PyObject* const* args, Py_ssize_t given, Py_ssize_t want) : a(args), n(given) {
         if (given != want) {
@@ -89,7 +91,8 @@ struct Args {
             PyErr_Format(PyExc_ValueError, "%s is on %s, not on a GPU", name, t.device().str().c_str());
             throw Fail{};
         }
-        if (t.device().index() != c10::cuda::current_device()) {
+        if (device < 0) device = c10::cuda::current_device();
+        if (t.device().index() != device) {
             PyErr_Format(PyExc_ValueError, "%s is on %s, not on the current device", name, t.device().str().c_str());
             throw Fail{};
         }
