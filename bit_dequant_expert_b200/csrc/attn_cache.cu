@@ -130,7 +130,10 @@ enum Kind { kQuery, kKey, kValue };
 // and a scaling an element (in pairs of fp32, one instruction for two).  With
 // a lane's place in the token's heads, the kind of head and the angles worked
 // out anew for each row the kernel was bound by its instructions (16384 tokens
-// of 20 heads of 128: 250 instructions a warp and 2 rows, 48 us).
+// of 20 heads of 128: 250 instructions a warp and 2 rows, 48 us; now 38 us, 4.6
+// TB/s, with 58% of the issue slots taken).  Five blocks a multiprocessor: with
+// six the registers spill (2048 tokens of 20 heads of 256 in 8 bits: 12.0 us
+// with five, 13.7 with six; the 16384 tokens 37.0 and 35.7).
 template <int D, bool kE4m3, bool kHalf>
 __global__ void __launch_bounds__(kPrepare, 5) k_attn_prepare(const AttnPrepareArgs a, int parts, int page_shift) {
     constexpr int L = D / 8, R = 32 / L;
@@ -289,7 +292,9 @@ constexpr int kReadUnroll = 2;  // units a thread has in flight, K's and V's of 
 // additions, as the kernel is bound by its instructions next to its bytes
 // (65k rows of 2 heads of 128 in 8 bits, 100 MB: 16.5 us, 6.1 TB/s; K's units
 // and then V's: 19.8).  Eight codes a lane, so that a warp's stores are whole
-// lines.  Two units at once (four: 19.4).
+// lines.  Two units at once (four: 19.4).  The cache's rows are not needed
+// again soon and leave L2 first, which then holds more of the outputs (with
+// these written back, call after call: 21.9 us, without 22.5).
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, int rows, int step_t, int step_h, int page_shift) {
     constexpr int L = D / 8, kUnroll = kReadUnroll;
@@ -334,8 +339,8 @@ __global__ void __launch_bounds__(kThreads) k_attn_read(const AttnReadArgs a, in
             scale[n][0] = scale[n][1] = 0.0f;
             if (row >= 0) {
                 const int64_t at = row + ((int64_t)h << page_shift);
-                w[n][0] = __ldg(static_cast<const Piece*>(a.cache.k) + at * L + l);
-                w[n][1] = __ldg(static_cast<const Piece*>(a.cache.v) + at * L + l);
+                w[n][0] = __ldcs(static_cast<const Piece*>(a.cache.k) + at * L + l);
+                w[n][1] = __ldcs(static_cast<const Piece*>(a.cache.v) + at * L + l);
                 if (kE4m3) scale[n][0] = __ldg(a.cache.ks + at), scale[n][1] = __ldg(a.cache.vs + at);
             }
             t += step_t, h += step_h;

@@ -31,6 +31,13 @@
 // largest at 2^7 or more: it is rounded to f16, 2^-12 of itself or 2^-32 of the
 // largest.  (The largest may be that of a row of zeros, whose scale is 1 by
 // the cache's definition beside much smaller ones: the 7 bits are theirs.)
+//
+// One sequence of 131072 rows of 2 heads of 256 in 8 bits: 27.7 us (4.9 TB/s),
+// 33.7 with the join.  64 ragged sequences up to 16384 of 2 heads of 128 in 8
+// bits, 32 query rows a head: 91 us (3.1 TB/s), with the mma pipe, the issue
+// slots and the shared memory each busy 37 to 43% of the time: a tile's steps
+// wait for one another.  (More groups, or the queries in registers instead of
+// shared memory: 56 us against 51 at half the lengths.)
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -48,8 +55,8 @@ namespace {
 constexpr int kTile = 64;            // keys of a tile
 constexpr int kSms = 148;
 constexpr int kProducers = 2;        // loading warps
-constexpr int kUnitCost = 4;         // of beginning and ending a head's pass, in tiles (0: 62 ragged sequences of 2 heads of 256, 8
-                                     // rows each, took 63 us; 2: 41; 4: 36; 6: 37)
+constexpr int kUnitCost = 4;         // of beginning and ending a head's pass, in tiles (62 ragged sequences up to 1000 of 2 heads of
+                                     // 256 in 8 bits, 8 rows each: 0 19.5 us; 2 16.8; 4 15.5; 6 15.5)
 constexpr int kMinPlaces = 2;        // places of a run at least (some then hold no tile)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;

@@ -25,6 +25,11 @@
 // one thread issues the tcgen05.mma and commits; warp 17: one thread issues
 // the TMA loads into a ring of slots; the last two idle.
 // Every wait is bounded (error word MOE_ERR_TIMEOUT, never a hang).
+//
+// Bound by the tensor pipe together with the exponentials, one in 8 clocks of a
+// scheduler: one causal prompt of 16384 tokens, 16 and 2 heads of 128, takes 1.02
+// ms under the power cap (1,075 TFLOP/s; the pipe runs 61% of the time), chunks of
+// 2048 and 1000 tokens after 8192 and 3999, heads of 256, 0.349 ms (1,098; 73%).
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -659,10 +664,13 @@ cudaError_t prefill_dim(const AttnPrefillArgs& a, cudaStream_t st) {
         return prefill_mode<D, kTurns>(a, st);
     } else {
         // Halves where pairs would leave the device half empty, or fill it hardly once with long rows of keys: the last
-        // tile then takes half as long.  B200, us (halves, pairs), 16 and 2 heads of 128: one prompt of 300 tokens 12, 15;
-        // 2048: 34, 45; 3000: 71, 78; 4096: 95, 81; four of 512: 22, 18; sixteen of 200: 40, 25.
+        // tile then takes half as long.  The lengths are on the device: of several sequences one is taken to hold half of
+        // all keys.  B200, us (halves, pairs), 16 and 2 heads of 128: one prompt of 300 tokens 10, 13; 2048: 34, 73; 3000:
+        // 66, 77; 3200: 68, 77; 4096: 90, 83; 8192: 268, 251.  Two of 1000: 26, 30; of 2000, 20 and 5: 40, 73; of 1500, 100,
+        // 30 and 700: 37, 49.  Four of 512: 22, 18; three of 600: 22, 19; sixteen of 200: 39, 25.  (Lost by it: three of
+        // 700: 30, 22; two of 1200: 41, 36.)
         const int64_t pairs = most_items(a, 2);
-        const bool halves = 2 * pairs <= 148 || (pairs < 200 && a.total_k >= (int64_t)1024 * a.B);
+        const bool halves = 2 * pairs <= 148 || (pairs < 212 && a.total_k >= (int64_t)1000 * std::min(a.B, 2));
         return halves ? prefill_mode<D, kHalves>(a, st) : prefill_mode<D, kPairs>(a, st);
     }
 }
