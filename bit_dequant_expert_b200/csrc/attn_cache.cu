@@ -390,9 +390,11 @@ template <int D>
 cudaError_t prepare_dim(const AttnPrepareArgs& a, cudaStream_t st) {
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // a token's heads in as many parts as it takes to give each multiprocessor eight warps, one warp-wide load at least
+    // a token's heads in as many parts as it takes to give each multiprocessor sixteen of the twenty warps it holds, one
+    // warp-wide load at least (B200, us with 8, 16 and 24, 20 heads of 128 in 8 bits: 256 tokens 5.3, 5.0, 4.6; 400: 5.7,
+    // 5.1, 7.4; 600: 7.2, 6.0, 7.0; 1000: 7.5, 6.3, 9.7; 2048: 9.0 each; 600 of 48 heads in 16 bits: 8.5, 5.7, 7.7)
     const int H = a.c.q_heads + 2 * a.c.kv_heads, most = (H * (D / 8) + 31) / 32;
-    const int parts = std::max(1, std::min(most, 8 * sms / a.T));
+    const int parts = std::max(1, std::min(most, 16 * sms / a.T));
     const int64_t blocks = ((int64_t)a.T * parts + kPrepare / 32 - 1) / (kPrepare / 32);
     auto kern = a.c.cache_type == ATTN_CACHE_E4M3
                     ? (a.layout == ATTN_ROPE_HALF ? k_attn_prepare<D, true, true> : k_attn_prepare<D, true, false>)
