@@ -165,7 +165,9 @@ int32_t attn_prefill(const attn_config_t* cfg, int32_t B, int32_t total_q, int32
  *   out, lse   as attn_prefill, B nq rows.
  *   ws         scratch of attn_decode_workspace_size bytes; needs no
  *              initialisation and keeps nothing between calls.
- * Rows of a page past the sequence's end may hold anything.
+ * Rows of a page past the sequence's end may hold anything.  A non-finite
+ * key or value in the sequence reaches its own tokens only, of the new ones
+ * those before it too.
  */
 size_t attn_decode_workspace_size(const attn_config_t* cfg, int32_t B, int32_t nq, int32_t max_len);
 int32_t attn_decode(const attn_config_t* cfg, int32_t B, int32_t nq, int32_t max_len, const uint16_t* q,
