@@ -472,6 +472,28 @@ def test_decode_long_runs_from_cold_memory(nq, dim, e4m3):
         R.check_attention(first[0][r].cpu(), first[1][r].cpu(), ref)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("nq,hq,hkv", [(8, 64, 1), (1, 256, 4), (3, 256, 256)])
+def test_decode_most_heads(nq, hq, hkv, dim, e4m3):
+    """The largest counts of heads and of query rows of one key head."""
+    run_decode([70, 0, 300], nq, hq, hkv, dim, e4m3, 16, seed=hq + nq)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_cache_most_heads(dim, e4m3):
+    for T, hq, hkv in ((1, 256, 256), (70, 256, 4), (5, 64, 64)):
+        test_prepare(T, hq, hkv, dim, dim, T % 2, e4m3, 16, {})
+        test_read([T, 0, 33], hkv, dim, e4m3, 16)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(64, 1), (256, 4), (256, 256)])
+def test_prefill_most_heads(hq, hkv, dim):
+    run_prefill([5, 0, 140], [5, 3, 200], hq, hkv, dim, True, seed=hq)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("nq", [1, 4])
 def test_decode_small_values_beside_rows_of_zeros(nq, dim):
