@@ -75,7 +75,9 @@ struct Smem {
     uint8_t slot[C::kSlots][C::kSlot];
     float m[2][kM], top[2][kM];                               // a group's maxima, handed on; between a row's threads
     uint64_t q_full, slot_full[C::kSlots], slot_empty[C::kSlots];
-    uint64_t s_full[2], p_half[2], p_full[2], o_done[2], m_full[2];   // p_half: the first 32 of each 64 keys
+    // of each score buffer; p_half: the first 32 of each 64 keys; o_done: the product of its probabilities.  A wait tells a
+    // phase from the next one only: each wait below is for the phase after one that its thread knows to be complete
+    uint64_t s_full[2], p_half[2], p_full[2], o_done[2], m_full[2];
     uint32_t tmem_base;
     int dead;                                                 // a bounded wait expired: every role leaves
     int find[24];                                             // scan of the work list; the block's item
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            add || part + i != 0);
                         }
                     }
-                    tc_commit_warp(issue, &sm.o_done[s]);
+                    tc_commit_warp(issue, &sm.o_done[buf]);
                 };
                 // values past the last key any row of the block sees are zeroed: they may hold NaN, and 0 NaN is NaN
                 auto zero_tail = [&](int first) {
@@ -497,8 +499,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kMode != kTurns) l *= f;
                 m = mn;
                 if ((kMode == kTurns ? j > 0 : n > 0) && __any_sync(0xFFFFFFFFu, f != 1.0f)) {
-                    ok = ok && mbar_wait_live(&sm.o_done[kMode == kTurns ? 0 : grp], (kMode == kTurns ? j - 1 : n - 1) & 1,
-                                              &sm.dead, a.err);
+                    // the last product into O: the group's own, n - 1, or in turns the other group's, of block j - 1.  Each
+                    // is the next phase there: this block's scores were asked for after the group's product before it, so
+                    // (turns) after the other group's of block j - 3
+                    ok = ok && mbar_wait_live(&sm.o_done[kMode == kTurns ? grp ^ 1 : grp],
+                                              (kMode == kTurns ? (j - 1) >> 1 : n - 1) & 1, &sm.dead, a.err);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     tc_fence_after();
                     if (ok) rescale_row<D / 2>(o_addr + half * (D / 2), f);
@@ -579,9 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // columns of this thread: half of the tile's, or a quarter where both groups hold the row
             constexpr int kCols = kMode == kPairs ? D / 2 : D / 4 < 32 ? 32 : D / 4;
             const int c0 = (kMode == kPairs ? half : 2 * grp + half) * kCols;
+            // the last phase of a group's o_done is the next one: the group's wait for its last block's scores said that
+            // its product before was done, and barrier 15 passes that on to the other group's threads.  In turns the last
+            // product's arrival says that all before it are done
             if (kMode == kHalves) {
                 ok = mbar_wait_live(&sm.o_done[0], ((blocks + 1) / 2 - 1) & 1, &sm.dead, a.err);
                 if (blocks > 1) ok = ok && mbar_wait_live(&sm.o_done[1], (blocks / 2 - 1) & 1, &sm.dead, a.err);
+            } else if (kMode == kTurns) {
+                ok = mbar_wait_live(&sm.o_done[(blocks - 1) & 1], ((blocks - 1) >> 1) & 1, &sm.dead, a.err);
             } else {
                 ok = mbar_wait_live(&sm.o_done[s], (blocks - 1) & 1, &sm.dead, a.err);
             }

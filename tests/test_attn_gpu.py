@@ -329,6 +329,51 @@ def test_prefill_neighbours_do_not_leak(dim):
     assert outs[1][101:161].isnan().all()
 
 
+def cold_prefills(lens_q, lens_k, hq, hkv, dim, causal, seed, repeats=6, data=None, scale=None):
+    """The same call again and again, each time after 256 MB were read, so that
+    its loads arrive at uneven times: each gives the same bits, and what the
+    definition says."""
+    g = rng(seed)
+    q = (torch.randn(sum(lens_q), hq, dim, generator=g) * 1.5).bfloat16()
+    k = (torch.randn(sum(lens_k), hkv, dim, generator=g) * 1.5).bfloat16()
+    v = torch.randn(sum(lens_k), hkv, dim, generator=g).bfloat16()
+    if data:
+        data(q, k)
+    scale = dim ** -0.5 if scale is None else scale
+    c, cu_q, cu_k = m.attn_config(hq, hkv, dim), R.starts(lens_q), R.starts(lens_k)
+    qd, kd, vd, cq, ck = R.cuda(q, k, v, cu_q, cu_k)
+    err, cold, first = err_word(), torch.zeros(64 << 20, device="cuda"), None
+    for _ in range(repeats):
+        cold.sum()                                       # more than the cache holds
+        out = torch.full(q.shape, math.nan, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(q.shape[:2], math.nan, device="cuda")
+        m.attn_prefill(c, len(lens_q), q.shape[0], k.shape[0], cq, ck, qd, hq * dim, kd, hkv * dim, vd, hkv * dim, scale,
+                       causal, out, lse, err=err)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        if first is None:
+            first = (out, lse)
+            for b in range(len(lens_q)):
+                r, s = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+                ref = R.attend(q[r], k[s], v[s], scale, prefill_limit(lens_q[b], lens_k[b], causal))
+                R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens_q,lens_k,hq,hkv", [
+    ([256], [256], 48, 48),                              # two blocks of keys
+    ([140, 5], [200, 5], 256, 256),
+    ([1, 128, 129, 300, 400, 640, 700], [1, 128, 129, 300, 400, 640, 700], 24, 24),   # one to six blocks
+    ([130, 257], [700, 511], 64, 8),                     # chunks after a prefix
+    ([300], [300], 8, 2),                                # few tiles
+    ([640], [760], 4, 4),
+])
+def test_prefill_from_cold_memory(lens_q, lens_k, hq, hkv, dim, causal):
+    cold_prefills(lens_q, lens_k, hq, hkv, dim, causal, seed=sum(lens_k) + dim)
+
+
 def test_prefill_reports_bad_boundaries():
     c = m.attn_config(2, 1, 64)
     q, k = torch.ones(20, 2, 64, device="cuda").bfloat16(), torch.ones(20, 1, 64, device="cuda").bfloat16()
