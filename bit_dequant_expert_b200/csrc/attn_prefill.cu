@@ -557,10 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = (int64_t)(w.q0 + row) * a.c.q_heads + (s ? w.head[1] : w.head[0]);
         uint16_t* out = a.out + at * D;
         if (kMode == kTurns && blocks > 0) {
-            const int last = (blocks - 1) & 1;                  // whose maximum is the last
-            if (last != grp) ok = ok && mbar_wait_live(&sm.m_full[last], ((blocks - 1) >> 1) & 1, &sm.dead, a.err);
-            m = sm.m[last][r];
-            if (m != m_own) l *= ex2(m_own - m);
+            // the group of the last block holds the last maximum; the other one is told, as before each of its blocks
+            // (threads of the first group do not read it: the row's other thread may have written it just now)
+            const int last = (blocks - 1) & 1;
+            if (last != grp) {
+                ok = ok && mbar_wait_live(&sm.m_full[last], ((blocks - 1) >> 1) & 1, &sm.dead, a.err);
+                m = sm.m[last][r];
+                if (m != m_own) l *= ex2(m_own - m);
+            }
         }
         if (kMode == kTurns) named_barrier(15, 512); else named_barrier(pair, 64);   // all have read it
         (half ? sm.top : sm.m)[grp][r] = l;

@@ -374,6 +374,22 @@ def test_prefill_from_cold_memory(lens_q, lens_k, hq, hkv, dim, causal):
     cold_prefills(lens_q, lens_k, hq, hkv, dim, causal, seed=sum(lens_k) + dim)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("high", range(1, 6))
+def test_prefill_maximum_moves_before_the_last_block(dim, high):
+    """Scores are 0 but in one block of keys, where they are some 30 above: of
+    the row's maxima only that block's moves, and every later block, the last
+    one too, works with the maximum that it was handed."""
+    def raised(q, k):
+        q[:], k[:] = 0, 0
+        q[..., 0] = 4
+        k[high * 128 - 100:high * 128, :, 0] = 8 + torch.rand(100, k.shape[1]).bfloat16()
+
+    blocks = high + 1
+    cold_prefills([128], [blocks * 128 - 3], 148, 148, dim, False, high, data=raised, scale=1.0)
+    cold_prefills([200, 128], [700, blocks * 128], 64, 8, dim, False, high, data=raised, scale=1.0)
+
+
 def test_prefill_reports_bad_boundaries():
     c = m.attn_config(2, 1, 64)
     q, k = torch.ones(20, 2, 64, device="cuda").bfloat16(), torch.ones(20, 1, 64, device="cuda").bfloat16()
