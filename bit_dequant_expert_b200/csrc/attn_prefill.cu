@@ -281,6 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k = kMode == kPairs ? j + 1 : j + 2;
                     if (k < nb) load_k(k);
                 }
+                // the block's shared memory may be another's once it leaves: the products' last arrivals come before
+                for (int i = max(0, n - C::kSlots); i < n && ok; ++i)
+                    ok = mbar_wait_live(&sm.slot_empty[i % C::kSlots], (i / C::kSlots) & 1, &sm.dead, a.err);
                 if (!ok) {   // leave no copy in flight behind
                     for (int i = max(0, n - C::kSlots); i < n; ++i)
                         mbar_wait_bounded(&sm.slot_full[i % C::kSlots], (i / C::kSlots) & 1, nullptr);

@@ -383,11 +383,29 @@ def test_prefill_maximum_moves_before_the_last_block(dim, high):
     def raised(q, k):
         q[:], k[:] = 0, 0
         q[..., 0] = 4
-        k[high * 128 - 100:high * 128, :, 0] = 8 + torch.rand(100, k.shape[1]).bfloat16()
+        k[high * 128 - 100:high * 128, :, 0] = (8 + torch.arange(100)[:, None] / 128).bfloat16()
 
     blocks = high + 1
     cold_prefills([128], [blocks * 128 - 3], 148, 148, dim, False, high, data=raised, scale=1.0)
     cold_prefills([200, 128], [700, blocks * 128], 64, 8, dim, False, high, data=raised, scale=1.0)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_calls_in_a_row(dim):
+    """Hundreds of short blocks after one another on each multiprocessor, call
+    upon call: the same bits in every one."""
+    hq, hkv, lens = 48, 24, [130, 17, 128, 260, 1, 64] * 8
+    g = rng(dim)
+    cu = R.starts(lens).cuda()
+    q, k, v = ((torch.randn(sum(lens), h, dim, generator=g)).bfloat16().cuda() for h in (hq, hkv, hkv))
+    c, err = m.attn_config(hq, hkv, dim), err_word()
+    outs = [torch.full(q.shape, math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(12)]
+    for out in outs:
+        m.attn_prefill(c, len(lens), q.shape[0], q.shape[0], cu, cu, q, hq * dim, k, hkv * dim, v, hkv * dim, dim ** -0.5,
+                       True, out, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.isfinite(outs[0].float()).all()
+    assert all(torch.equal(out, outs[0]) for out in outs[1:])
 
 
 def test_prefill_reports_bad_boundaries():
