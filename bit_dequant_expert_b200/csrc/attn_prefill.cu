@@ -85,10 +85,11 @@ struct Smem {
 
 // What a block works on: query rows [q0, q0 + lq) and keys [k0, k0 + lk) of a
 // sequence, and for each of its tiles the first row within the sequence, the
-// head and the number of key blocks (0: nothing but zeros, or no tile).
+// head, the keys that its last row sees and the number of their blocks (0:
+// nothing but zeros, or no tile).
 struct Work {
     int q0, lq, k0, lk;
-    int row[2], head[2], nb[2];
+    int row[2], head[2], seen[2], nb[2];
     bool live[2];
 };
 
@@ -233,10 +234,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             w.head[s] = kvh * G + u % G;
             int n = w.lk;
             if (a.causal) n = min(n, min(w.row[s] + kM, w.lq) + w.lk - w.lq);
-            w.nb[s] = w.live[s] && n > 0 ? (n + kN - 1) / kN : 0;
+            w.seen[s] = w.live[s] ? max(n, 0) : 0;
+            w.nb[s] = (w.seen[s] + kN - 1) / kN;
         }
     }
     const int nb = max(w.nb[0], w.nb[1]);
+    // a pair's first tile may be of earlier rows than the second (an odd number of heads) and see only a part of its last
+    // block of keys: that block's values are then loaded once more, so that each tile's can be zeroed past what it sees
+    // (-1: not so)
+    const int apart = kMode == kPairs && w.seen[0] < w.seen[1] && w.seen[0] % kN ? w.nb[0] - 1 : -1;
 
     if (warp == 16) {
         tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -278,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (kMode != kPairs && nb > 1) load_k(1);
                 for (int j = 0; j < nb && ok; ++j) {
                     load_v(j);
+                    if (kMode == kPairs && j == apart) load_v(j);
                     const int k = kMode == kPairs ? j + 1 : j + 2;
                     if (k < nb) load_k(k);
                 }
@@ -295,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the whole warp runs in step (its conditions made uniform), one lane issues
             const bool issue = elect_lane();
             const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sm.tmem_base, 0);
-            const int nb0 = __shfl_sync(0xFFFFFFFFu, w.nb[0], 0), nb1 = __shfl_sync(0xFFFFFFFFu, w.nb[1], 0);
-            const int nb = max(nb0, nb1);
+            const int seen0 = __shfl_sync(0xFFFFFFFFu, w.seen[0], 0), seen1 = __shfl_sync(0xFFFFFFFFu, w.seen[1], 0);
+            const int nb0 = (seen0 + kN - 1) / kN, nb1 = (seen1 + kN - 1) / kN, nb = max(nb0, nb1);
             if (nb > 0) {
                 constexpr uint32_t kIdS = idesc_bf16_f32(kM, kN);
                 constexpr uint32_t kIdO = idesc_bf16_f32_bmn(kM, D);
@@ -331,8 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit_warp(issue, &sm.s_full[buf]);
                 };
                 // O `s` += P V, P in bf16 over the S buffer: each half of the keys over its own scores.  The softmax
-                // threads hand P over in two parts, the first 32 and the last 32 keys of each half.
-                auto product_o = [&](int s, int buf, int first, bool add, uint32_t parity) {
+                // threads hand P over in two parts, the first 32 and the last 32 keys of each half.  Of a tile's last block
+                // only the first `keys` rows of V count (in steps of 16; zero_tail has cleared the rest of the last step, in
+                // place of the whole rest: two of 2049 keys, 16 heads of 128, 50.3 us instead of 57.4).
+                auto product_o = [&](int s, int buf, int first, bool add, uint32_t parity, int keys) {
                     constexpr int kKeys = kN / C::kParts;
                     const uint32_t d = tmem + C::kOCol + s * D, pa = tmem + buf * kN;
                     uint32_t vb[C::kParts];
@@ -345,33 +354,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                           &sm.dead, a.err));
                         tc_fence_after();
                         if (!ok) return;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        auto step = [&](bool go, int i) {
                             const int kk = (i & 1) + (i >> 1) * 4 + part * 2;
-                            tc_mma_ts_warp(issue, d, pa + kk / 4 * 64 + kk % 4 * 8,
+                            tc_mma_ts_warp(go && issue, d, pa + kk / 4 * 64 + kk % 4 * 8,
                                            vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi, kIdO,
                                            add || part + i != 0);
+                        };
+                        // head size 64 branches, whose products are too short to hide a comparison each (16 and 2 heads, 8192
+                        // tokens: 206.9 us, with the comparisons alone 216; of 128: 230 with the branch, 227.9 without)
+                        if (D == 64 && keys >= kN) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) step(true, i);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) step(((i & 1) + (i >> 1) * 4 + part * 2) * 16 < keys, i);
                         }
                     }
                     tc_commit_warp(issue, &sm.o_done[buf]);
                 };
-                // values past the last key any row of the block sees are zeroed: they may hold NaN, and 0 NaN is NaN
-                auto zero_tail = [&](int first) {
-                    int seen = w.lk;
-                    if (a.causal) {
-                        const int last = max(w.live[0] ? min(w.row[0] + kM, w.lq) : 0, w.live[1] ? min(w.row[1] + kM, w.lq) : 0);
-                        seen = min(seen, last + w.lk - w.lq);
-                    }
-                    const int from = seen - (nb - 1) * kN;   // rows of the last block that stay
+                // values past the last key that the tile sees, from this row of its last block to the end of the step of 16
+                // that holds it, are zeroed: they may hold NaN, and 0 NaN is NaN
+                auto zero_tail = [&](int first, int from) {
                     constexpr int kKeys = kN / C::kParts;
-                    if (from >= kN) return;
-                    for (int p = 0; p < C::kParts; ++p) {
-                        const int lo = max(0, from - p * kKeys), rows = kKeys - lo;
-                        uint8_t* base = sm.slot[(first + p) % C::kSlots];
-                        for (int i = lane; i < rows * (D / 8); i += 32) {
-                            const int panel = i / (rows * 8), r = i % (rows * 8);
-                            *reinterpret_cast<uint4*>(base + panel * (kKeys * 128) + lo * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-                        }
+                    uint8_t* base = sm.slot[(first + from / kKeys) % C::kSlots];
+                    const int lo = from % kKeys, rows = -from & 15;
+                    for (int i = lane; i < rows * (D / 8); i += 32) {
+                        const int panel = i / (rows * 8), r = i % (rows * 8);
+                        *reinterpret_cast<uint4*>(base + panel * (kKeys * 128) + lo * 128 + r * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_shared();
                     __syncwarp();
@@ -385,13 +394,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if ((s ? nb1 : nb0) > 0) product_s(s, s, kf);
                         release(kf);
                     }
+                    const int split = __shfl_sync(0xFFFFFFFFu, apart, 0);
                     for (int j = 0; j < nb && ok; ++j) {
-                        const int vf = take();
-                        if (j == nb - 1 && ok) zero_tail(vf);
+                        int vf = take();
+                        if ((j == split || j == nb - 1) && ok) zero_tail(vf, (j == split ? seen0 : max(seen0, seen1)) - j * kN);
                         bool have = false;
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            if (j < (s ? nb1 : nb0) && ok) product_o(s, s, vf, j > 0, j & 1);
+                            if (j < (s ? nb1 : nb0) && ok) product_o(s, s, vf, j > 0, j & 1, (s ? seen1 : seen0) - j * kN);
+                            if (s == 0 && j == split) {   // the second tile's copy
+                                release(vf);
+                                vf = take();
+                                if (j == nb - 1 && ok) zero_tail(vf, seen1 - j * kN);
+                            }
                             if (j + 1 < (s ? nb1 : nb0) && ok) {
                                 if (!have) kf = take();
                                 have = true;
@@ -413,8 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     for (int j = 0; j < nb && ok; ++j) {
                         const int vf = take(), g = j & 1;
-                        if (j == nb - 1 && ok) zero_tail(vf);
-                        if (ok) product_o(kMode == kHalves ? g : 0, g, vf, kMode == kHalves ? j > 1 : j > 0, (j >> 1) & 1);
+                        if (j == nb - 1 && ok) zero_tail(vf, seen0 - j * kN);
+                        if (ok)
+                            product_o(kMode == kHalves ? g : 0, g, vf, kMode == kHalves ? j > 1 : j > 0, (j >> 1) & 1,
+                                      seen0 - j * kN);
                         if (!ok) break;
                         release(vf);
                         if (j + 2 < nb) {

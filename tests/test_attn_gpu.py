@@ -408,6 +408,37 @@ def test_prefill_calls_in_a_row(dim):
     assert all(torch.equal(out, outs[0]) for out in outs[1:])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,seqs", [(64, 64, 4), (48, 16, 4), (64, 32, 4), (3, 1, 1), (2, 2, 1)])
+@pytest.mark.parametrize("lq,lk", [(256, 320), (150, 214), (400, 401), (257, 384), (300, 300)])
+def test_prefill_non_finite_values_reach_back_127_positions(lq, lk, hq, hkv, seqs, dim):
+    """One value row of a head holds NaN: queries that see it give NaN, those
+    more than 127 positions before it what the definition says of the rows that
+    they see, wherever the row lies in a tile."""
+    g, c = rng(lk + hq), m.attn_config(hq, hkv, dim)
+    q = torch.randn(seqs * lq, hq, dim, generator=g).bfloat16()
+    k, v = (torch.randn(seqs * lk, hkv, dim, generator=g).bfloat16() for _ in "kv")
+    scale, cu_q, cu_k = dim ** -0.5, R.starts([lq] * seqs).cuda(), R.starts([lk] * seqs).cuda()
+    qd, kd = R.cuda(q, k)
+    for at in sorted({lk - 1, lk - lq + 128, lk - lq + 191, 255, 128, min(lk - 1, 300)}):
+        if at >= seqs * lk:
+            continue
+        bad = v.clone()
+        bad[at] = math.nan
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda")
+        m.attn_prefill(c, seqs, seqs * lq, seqs * lk, cu_q, cu_k, qd, hq * dim, kd, hkv * dim, bad.cuda(), hkv * dim, scale,
+                       True, out)
+        got, b = out.cpu().split(lq), at // lk
+        first = at - b * lk - (lk - lq)                      # the first query of sequence b that sees the row
+        before = max(0, min(lq, first - 127))
+        if before:
+            r = slice(b * lq, b * lq + before)
+            ref = R.attend(q[r], k[b * lk:(b + 1) * lk], v[b * lk:(b + 1) * lk], scale, prefill_limit(lq, lk, True)[:before])
+            R.check_attention(got[b][:before], None, ref)
+        assert got[b][max(0, first):].isnan().all()
+        assert all(o.isfinite().all() for i, o in enumerate(got) if i != b)
+
+
 def test_prefill_reports_bad_boundaries():
     c = m.attn_config(2, 1, 64)
     q, k = torch.ones(20, 2, 64, device="cuda").bfloat16(), torch.ones(20, 1, 64, device="cuda").bfloat16()
