@@ -12,6 +12,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -27,6 +28,7 @@ BUILD = os.path.join(HERE, "_build")
 OUT = os.path.join(HERE, "libmoe_b200.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(HERE, "_attn_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_FOR = os.path.join(BUILD, "attn_binding.built_for")   # what the module beside it was built for
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -60,26 +62,46 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in sources() + _deps())
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def binding_for() -> str:
+    """What the extension module's binary interface hangs on besides its sources: Python, torch (which one and where) and
+    the compiler."""
+    cxx = subprocess.check_output([_cxx(), "--version"], text=True).splitlines()[0]
+    return "\n".join((sys.version, importlib.metadata.version("torch"), _torch_dir(), cxx)) + "\n"
+
+
 def binding_stale() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
         return True
+    with open(BINDING_FOR) as f:
+        if f.read() != binding_for():
+            return True
     t = os.path.getmtime(BINDING)
     return any(os.path.getmtime(p) > t for p in (BINDING_SRC, os.path.join(INCLUDE, "attn_b200.h")))
 
 
 def build_binding() -> None:
     """The extension module: host code only, linked to the library beside it and to torch's own libraries."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch_dir = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     libs = os.path.join(torch_dir, "lib")
     tmp = BINDING + ".tmp.%d" % os.getpid()
     subprocess.check_call(
-        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
+        [_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp, "-I", INCLUDE,
          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(torch_dir, "include"),
          "-I", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
          "-L", HERE, "-l:libmoe_b200.so", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
          "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs], env=_env())
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(binding_for())
 
 
 def _env() -> dict:
