@@ -10,7 +10,9 @@ module, ``_attn_binding``, which also checks their tensors' device, type and
 layout.
 
 Importing fails loudly when the library has not been built; there is no
-fallback implementation.
+fallback implementation.  Where only ``_attn_binding`` cannot be loaded (it is
+built for one torch), the attention calls raise that ImportError and the others
+run.
 """
 from __future__ import annotations
 
@@ -28,7 +30,22 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _attn_binding as _attn  # noqa: E402  (the attention calls, without ctypes' cost per argument)
+
+class _Unloaded:
+    """In place of a module that could not be loaded: every use raises why."""
+
+    def __init__(self, error: ImportError):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError("%s is not available: %s (run `python bit_dequant_expert_b200/build.py`)"
+                          % (name, self._error)) from self._error
+
+
+try:
+    from . import _attn_binding as _attn  # the attention calls, without ctypes' cost per argument
+except ImportError as _e:
+    _attn = _Unloaded(_e)
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
