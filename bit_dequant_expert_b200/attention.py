@@ -159,7 +159,9 @@ class AttentionLayer:
             return out
 
     def check(self) -> None:
-        """Raises what a kernel reported since the last check (waits for the device)."""
+        """Raises what a kernel reported since the last check (waits for the device: the layer's calls may be on any
+        stream)."""
+        torch.cuda.synchronize(self.device)
         status = int(self.err.item())
         if status:
             self.err.zero_()

@@ -851,6 +851,27 @@ def test_layer_refusals():
     L.check()
 
 
+def test_layer_check_waits_for_every_stream():
+    """An error of a call on another stream, still to run when check() is
+    called, is raised by that check and not by a later one."""
+    _, L, *_ = layer_case(False)
+    rows = torch.zeros(4, L.row, dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(4, dtype=torch.int32, device="cuda")
+    args = (rows, z, z + L.num_pages * 32, z[:, None].contiguous(), z + 1, 32)
+    L.decode(rows, z, z, *args[3:])
+    big = torch.zeros(256 << 20, device="cuda")
+    L.check()
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        for _ in range(60):
+            big.add_(1.0)                                    # some 20 ms of work before the call
+        L.decode(*args)                                      # slots outside the cache
+    with pytest.raises(m.MoeError, match="MOE_ERR_BOUNDS"):
+        L.check()
+    torch.cuda.synchronize()
+    L.check()
+
+
 # ------------------------------------------------------------------ the binding, streams
 
 
