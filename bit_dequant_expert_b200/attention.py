@@ -117,6 +117,8 @@ class AttentionLayer:
                 self._check(cu_k, "cu_k", torch.int32, (B + 1,))
                 if total_k is None or total_k < 0:
                     raise ValueError("total_k must be given with page_table")
+            elif cu_k is not None or total_k is not None:
+                raise ValueError("cu_k and total_k are of the cached rows: page_table must be given with them")
             q, k = self._prepare(qkv, positions, slots, keys=not cached)
             T = qkv.shape[0]
             if cached:

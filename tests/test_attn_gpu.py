@@ -851,6 +851,18 @@ def test_layer_refusals():
     L.check()
 
 
+def test_layer_prefill_refuses_cached_lengths_without_pages():
+    """Without the pages the prefix would be left out with no word of it."""
+    _, L, *_ = layer_case(False)
+    rows = torch.zeros(4, L.row, dtype=torch.bfloat16, device="cuda")
+    z, cu = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    for more in (dict(cu_k=cu), dict(total_k=4), dict(cu_k=cu, total_k=4)):
+        with pytest.raises(ValueError, match="page_table must be given"):
+            L.prefill(rows, z, z - 1, cu, **more)
+    L.prefill(rows, z, z - 1, cu)
+    L.check()
+
+
 def test_layer_check_waits_for_every_stream():
     """An error of a call on another stream, still to run when check() is
     called, is raised by that check and not by a later one."""
