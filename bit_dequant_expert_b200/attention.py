@@ -150,6 +150,8 @@ class AttentionLayer:
             self._check(page_table, "page_table", torch.int32, (B, None))
             if max_len < 1 or page_table.shape[1] * c.page_size < max_len:
                 raise ValueError("page_table rows of %d pages for %d tokens" % (page_table.shape[1], max_len))
+            if B > 1 and page_table.stride(0) < page_table.shape[1]:
+                page_table = page_table.contiguous()         # one row for all sequences, expanded
             nq = qkv.shape[0] // B
             q, _ = self._prepare(qkv, positions, slots, keys=False)
             out = torch.empty_like(q)

@@ -863,6 +863,27 @@ def test_layer_prefill_refuses_cached_lengths_without_pages():
     L.check()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_layer_steps_on_shared_pages(e4m3):
+    """One page table row expanded to all sequences (several continuations of
+    one prefix): what a table with the row repeated gives, in decode and in a
+    prompt's next chunk."""
+    g, L, *_ = layer_case(e4m3)
+    row = torch.randperm(L.num_pages, generator=g)[:6].int().cuda()
+    at = torch.arange(150, device="cuda")
+    slots = (row[at // 32] * 32 + at % 32).int()
+    L.prefill(torch.randn(150, L.row, generator=g).bfloat16().cuda(), at.int(), slots, R.starts([150]).cuda())
+    qkv, pos, none = torch.randn(3, L.row, generator=g).bfloat16().cuda(), torch.full((3,), 150).int().cuda(), torch.full((3,), -1).int().cuda()
+    lens = torch.tensor([150, 149, 33], dtype=torch.int32, device="cuda")
+    shared, repeated = row[None].expand(3, 6), row[None].repeat(3, 1)
+    outs = [L.decode(qkv, pos, none, t, lens, 160) for t in (shared, repeated)]
+    assert torch.equal(*outs) and torch.isfinite(outs[0].float()).all()
+    cu_q, cu_k = R.starts([1, 1, 1]).cuda(), R.starts([150, 149, 33]).cuda()
+    outs = [L.prefill(qkv, pos, none, cu_q, page_table=t, cu_k=cu_k, total_k=332) for t in (shared, repeated)]
+    assert torch.equal(*outs) and torch.isfinite(outs[0].float()).all()
+    L.check()
+
+
 def test_layer_check_waits_for_every_stream():
     """An error of a call on another stream, still to run when check() is
     called, is raised by that check and not by a later one."""
