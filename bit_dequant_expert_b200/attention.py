@@ -37,6 +37,8 @@ class AttentionLayer:
         if num_pages < 1:
             raise ValueError("num_pages must be at least 1, got %d" % num_pages)
         self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("the layer runs on a GPU, not on %s" % self.device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.num_pages, self.eps, self.rope_layout, self.rope_scale = num_pages, eps, rope_layout, rope_scale

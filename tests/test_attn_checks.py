@@ -151,3 +151,9 @@ def test_layer_refuses_bad_shapes():
         m.AttentionLayer(16, 2, 128, 4, q_weight=torch.ones(64), device="cuda:0")
     with pytest.raises(ValueError, match="inv_freq"):
         m.AttentionLayer(16, 2, 128, 4, inv_freq=torch.ones(12), device="cuda:0")
+
+
+@pytest.mark.parametrize("device", ["cpu", "meta", torch.device("cpu")])
+def test_layer_refuses_other_devices(device):
+    with pytest.raises(ValueError, match="runs on a GPU"):
+        m.AttentionLayer(16, 2, 128, 4, device=device)
