@@ -105,6 +105,7 @@ int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const i
     int32_t st = check_config(cfg);
     if (st) return st;
     if (B < 1 || total < 0 || page_table_stride < 1 || page_table_stride > kMaxStride) return MOE_ERR_INVALID_ARG;
+    if (total > 0x7FFFFF00) return MOE_ERR_UNSUPPORTED;   // rows are numbered in 31 bits, a block's past the last one too
     if (total == 0) return MOE_OK;
     if (!page_table || !cu_lens || !k_out || !v_out || !aligned(page_table, 4) || !aligned(cu_lens, 4) ||
         !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(err, 4))

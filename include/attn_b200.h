@@ -112,8 +112,8 @@ int32_t attn_qkv_prepare(const attn_config_t* cfg, int32_t T, const uint16_t* qk
  * n_b = cu_lens[b + 1] - cu_lens[b], and row j of sequence b goes to row
  * cu_lens[b] + j of the outputs.
  *   cu_lens    int32 [B + 1], not decreasing, cu_lens[0] >= 0.
- *   total      rows of k_out and v_out (>= 0; 0: nothing is done).  Rows
- *              outside [cu_lens[0], cu_lens[B]) are left as they are; rows
+ *   total      rows of k_out and v_out (0 .. 2^31 - 256; 0: nothing is done).
+ *              Rows outside [cu_lens[0], cu_lens[B]) are left as they are; rows
  *              past total are not written and reported (MOE_ERR_BOUNDS).
  *   page_table int32 rows of page indices, page_table_stride elements apart
  *              (1 .. 2^31; any value, not only multiples of 8), all of which

@@ -157,3 +157,8 @@ def test_layer_refuses_bad_shapes():
 def test_layer_refuses_other_devices(device):
     with pytest.raises(ValueError, match="runs on a GPU"):
         m.AttentionLayer(16, 2, 128, 4, device=device)
+
+
+def test_read_refuses_more_rows_than_it_can_number():
+    for total in (0x7FFFFF01, 0x7FFFFF81, 0x7FFFFFFF):
+        assert read(total=total) == UNS
