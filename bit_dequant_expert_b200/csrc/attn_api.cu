@@ -49,6 +49,9 @@ AttnCache cache_of(const attn_config_t* c, int32_t num_pages, const void* k, con
 
 constexpr int64_t kMaxStride = (int64_t)1 << 31;   // elements; offsets of 2^31 rows then fit 64 bits
 
+// Scores are multiplied by scale log2 e, which must not be infinite: a score of zero would become NaN.
+bool scale_ok(float scale) { return std::isfinite(scale * 1.4426950408889634f); }
+
 bool row_stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= kMaxStride; }
 
 }  // namespace
@@ -134,7 +137,7 @@ int32_t attn_prefill(const attn_config_t* cfg, int32_t B, int32_t total_q, int32
     int32_t st = check_config(cfg);
     if (st) return st;
     const int64_t q_row = (int64_t)cfg->q_heads * cfg->head_dim, kv_row = (int64_t)cfg->kv_heads * cfg->head_dim;
-    if (B < 1 || total_q < 1 || total_k < 0 || (causal != 0 && causal != 1) || !std::isfinite(scale))
+    if (B < 1 || total_q < 1 || total_k < 0 || (causal != 0 && causal != 1) || !scale_ok(scale))
         return MOE_ERR_INVALID_ARG;
     if (!cu_q || !cu_k || !q || !out || (total_k && (!k || !v))) return MOE_ERR_INVALID_ARG;
     if (!row_stride_ok(q_stride, q_row) || !row_stride_ok(k_stride, kv_row) || !row_stride_ok(v_stride, kv_row))
@@ -178,7 +181,7 @@ int32_t attn_decode(const attn_config_t* cfg, int32_t B, int32_t nq, int32_t max
     moe::ApiRange api_range("attn_decode");
     int32_t st = check_config(cfg);
     if (st) return st;
-    if (B < 1 || nq < 1 || max_len < 1 || !std::isfinite(scale) || !q || !page_table || !seq_lens || !out)
+    if (B < 1 || nq < 1 || max_len < 1 || !scale_ok(scale) || !q || !page_table || !seq_lens || !out)
         return MOE_ERR_INVALID_ARG;
     if (B > 65535 || nq > 8) return MOE_ERR_UNSUPPORTED;
     if (!row_stride_ok(q_stride, (int64_t)cfg->q_heads * cfg->head_dim)) return MOE_ERR_INVALID_ARG;

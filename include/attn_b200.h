@@ -137,7 +137,7 @@ int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const i
  *              reported and that sequence is skipped.  Rows of out and lse
  *              that belong to no sequence are left as they are.
  *   q, k, v    bf16 rows, the strides in elements.
- *   scale      finite, applied to q . k.
+ *   scale      finite, also times log2 e; applied to q . k.
  *   out        bf16 [total_q, q_heads, head_dim].
  *   lse        fp32 [total_q, q_heads] or NULL: log of the sum of the
  *              exponentials of the scaled scores.

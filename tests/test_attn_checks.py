@@ -162,3 +162,8 @@ def test_layer_refuses_other_devices(device):
 def test_read_refuses_more_rows_than_it_can_number():
     for total in (0x7FFFFF01, 0x7FFFFF81, 0x7FFFFFFF):
         assert read(total=total) == UNS
+
+
+def test_scales_that_overflow_in_log2_units_are_refused():
+    for scale in (2.4e38, -3e38):
+        assert prefill(scale=scale) == INV and decode(scale=scale) == INV
