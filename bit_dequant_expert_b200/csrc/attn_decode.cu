@@ -189,6 +189,16 @@ __device__ __forceinline__ float lg2(float x) {
     return r;
 }
 
+// y 2^d, f = 2^d, d <= 0, also where f is below the least fp32 number and y is large: sums of probabilities, whose maxima
+// follow the values' scales, are as far from one another as those (2^-80 .. 2^119).
+__device__ __forceinline__ float times_ex2(float y, float d, float f) {
+    if (d <= -120.0f) {
+        f = ex2(0.5f * d);
+        y *= f;
+    }
+    return y * f;
+}
+
 template <int D, bool kE4m3, int NT>
 __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
     k_attn_decode(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -628,8 +638,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
                                               fmaxf(sm.top[grp][2][row], sm.top[grp][3][row]));
                         if (x > m[r][e] + kGrow) {
                             const float n = x - kLead, f = ex2(m[r][e] - n);
+                            l[r][e] = kE4m3 ? times_ex2(l[r][e], m[r][e] - n, f) : l[r][e] * f;
                             m[r][e] = n;
-                            l[r][e] *= f;
 #pragma unroll
                             for (int i = 0; i < C::kCols; ++i) o[r][i][e] *= f, o[r][i][2 + e] *= f;
                         }
@@ -732,7 +742,8 @@ __global__ void __launch_bounds__(Cfg<D, kE4m3, NT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < C::kGroups; ++i) {
                 const float x = sm.m[i][row], y = (sm.l[i][0][row] + sm.l[i][1][row]) + (sm.l[i][2][row] + sm.l[i][3][row]);
-                L += x == -CUDART_INF_F ? y : y * ex2(x - M);
+                const float d = x == -CUDART_INF_F ? 0.0f : x - M;
+                L += times_ex2(y, d, ex2(d));
             }
             sm.fin[row][0] = M, sm.fin[row][1] = L;
         }
@@ -839,9 +850,10 @@ __global__ void __launch_bounds__(256) k_attn_combine(const AttnDecodeArgs a, co
                 }
                 const float m = fmaxf(M, ml.x);
                 // a run with no key seen holds zeros, or NaN
-                const float f = M == -CUDART_INF_F ? 1.0f : ex2(M - m), h = ml.x == -CUDART_INF_F ? 1.0f : ex2(ml.x - m);
+                const float df = M == -CUDART_INF_F ? 0.0f : M - m, dh = ml.x == -CUDART_INF_F ? 0.0f : ml.x - m;
+                const float f = ex2(df), h = ex2(dh);
+                L = times_ex2(L, df, f) + times_ex2(ml.y, dh, h);
                 M = m;
-                L = L * f + ml.y * h;
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -865,8 +877,8 @@ __global__ void __launch_bounds__(256) k_attn_combine(const AttnDecodeArgs a, co
                     for (int e = 0; e < kV; ++e) o[n][e] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float h = ms[i].x == -CUDART_INF_F ? 1.0f : ex2(ms[i].x - M);
-                    L += ms[i].y * h;
+                    const float d = ms[i].x == -CUDART_INF_F ? 0.0f : ms[i].x - M, h = ex2(d);
+                    L += times_ex2(ms[i].y, d, h);
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll

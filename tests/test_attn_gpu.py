@@ -633,6 +633,38 @@ def test_decode_small_values_beside_rows_of_zeros(nq, dim):
         R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[130], [700, 64], [9000]])
+@pytest.mark.parametrize("low,high", [(-86, 70), (-89, 100), (-40, 60)])
+def test_decode_values_of_very_different_scales(low, high, lens, dim):
+    """Rows of values near 2^low before, behind and between rows near 2^high,
+    all counting alike: the sums of the probabilities lose none of them."""
+    g, page, hkv, nq = rng(dim + high), 16, 2, 2
+    table, pages = R.make_table(g, lens, page)
+    kc, ks = R.quantised(torch.randn(pages, hkv, page, dim, generator=g))
+    v = torch.randn(pages, hkv, page, dim, generator=g)
+    exponent = torch.full((pages, hkv, page, 1), float(low))
+    for b, n in enumerate(lens):                          # tiles of 64 rows: low, high, low low high and so on
+        for j in range((n + page - 1) // page):
+            if j // 4 % 3 == 1:
+                exponent[table[b, j].long(), :, :] = high
+    v = v * torch.exp2(exponent)
+    vc, vs = R.quantised(v)
+    q = torch.zeros(len(lens) * nq, 16, dim, dtype=torch.bfloat16)
+    c, top = m.attn_config(16, hkv, dim, page, m.ATTN_CACHE_E4M3), max(lens)
+    ws = torch.empty(m.attn_decode_workspace_size(c, len(lens), nq, top), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    qd, tb, ln, kd, vd, ksd, vsd = R.cuda(q, table, torch.tensor(lens, dtype=torch.int32), kc, vc, ks, vs)
+    m.attn_decode(c, len(lens), nq, top, qd, 16 * dim, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, dim ** -0.5, out,
+                  lse, ws)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        r = slice(b * nq, b * nq + nq)
+        ref = R.attend(q[r], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), dim ** -0.5,
+                       [n - nq + i + 1 for i in range(nq)])
+        R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A bad page reads as zeros (score 0, value 0) and is reported; so is a
     length above max_len (cut) or below zero (none)."""
