@@ -40,7 +40,8 @@
  *    row of zeros), the code rounded to nearest even.  A row with a
  *    non-finite element gets a NaN scale: all of it reads as NaN.
  *    (attn_decode: beside a row of zeros, values below 2^-12 lose bits,
- *    as their scales fall below 2^-21 of its.)
+ *    as their scales fall below 2^-21 of its; so do, anywhere, values
+ *    below 2^-80, and those below 2^-102 may read as zeros.)
  *  - `err` (may be NULL): a device word for what only the device can see; the
  *    first error of any call stays in it until the caller clears it, and the
  *    kernel carries on with safe values.  MOE_ERR_BOUNDS: a slot, page or

@@ -665,6 +665,31 @@ def test_decode_values_of_very_different_scales(low, high, lens, dim):
         R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("exponent", [-80, -40, 60, 120])
+def test_decode_tiny_and_huge_values(exponent, dim):
+    """Values down to 2^-80 and up to the largest of bf16 keep their bits: the
+    bounds of check_attention in units of 2^exponent."""
+    g, page, hkv, nq, lens = rng(dim + exponent), 32, 2, 2, [500, 60]
+    table, pages = R.make_table(g, lens, page)
+    kc, ks = R.quantised(torch.randn(pages, hkv, page, dim, generator=g))
+    vc, vs = R.quantised(torch.randn(pages, hkv, page, dim, generator=g) * 2.0 ** exponent)
+    q = (torch.randn(len(lens) * nq, 16, dim, generator=g) * 1.5).bfloat16()
+    c, top = m.attn_config(16, hkv, dim, page, m.ATTN_CACHE_E4M3), max(lens)
+    ws = torch.empty(m.attn_decode_workspace_size(c, len(lens), nq, top), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(q.shape, dtype=torch.bfloat16, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+    qd, tb, ln, kd, vd, ksd, vsd = R.cuda(q, table, torch.tensor(lens, dtype=torch.int32), kc, vc, ks, vs)
+    m.attn_decode(c, len(lens), nq, top, qd, 16 * dim, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, dim ** -0.5, out,
+                  lse, ws)
+    torch.cuda.synchronize()
+    for b, n in enumerate(lens):
+        r = slice(b * nq, b * nq + nq)
+        o, z, A, big = R.attend(q[r], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), dim ** -0.5,
+                                [n - nq + i + 1 for i in range(nq)])
+        unit = 2.0 ** -exponent
+        R.check_attention(out[r].cpu().double() * unit, lse[r].cpu(), (o * unit, z, A * unit, big))
+
+
 def test_decode_reports_bad_pages_and_lengths():
     """A bad page reads as zeros (score 0, value 0) and is reported; so is a
     length above max_len (cut) or below zero (none)."""
