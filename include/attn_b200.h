@@ -26,9 +26,9 @@
  * Conventions:
  *  - All pointers are DEVICE pointers on the current device; the caller owns
  *    every buffer; nothing is allocated, no state is kept.  bf16 travels as
- *    uint16_t bits.  Every array of bf16, codes or scales and the workspace
- *    is 16-byte aligned, 32-bit index and fp32 arrays 4-byte aligned, except
- *    where a call says more.
+ *    uint16_t bits.  Every array of bf16, codes or scales is 16-byte aligned,
+ *    the workspace 256-byte aligned; the other arrays, of 32-bit integers and
+ *    fp32, 4-byte aligned.
  *  - Row strides count elements and are multiples of 8, up to 2^31; a row holds its heads
  *    one after another, [heads, head_dim].  Outputs are contiguous.
  *  - Paged cache: k_cache and v_cache [num_pages, kv_heads, page_size,
@@ -99,8 +99,10 @@ typedef struct attn_config {
  *              would mix both).  num_pages * page_size < 2^31.
  *   q_out      bf16 [T, q_heads, head_dim].
  *   k_out      bf16 [T, kv_heads, head_dim] or NULL.
- * Arithmetic is fp32, each output rounded once.  The outputs do not overlap
- * qkv.
+ * Arithmetic is fp32 (the angle's product fp64, its remainder rounded to fp32;
+ * the root's reciprocal multiplies last), each output rounded once; a code may
+ * so fall to the other side of a border that its quotient lies next to.  The
+ * outputs do not overlap qkv.
  */
 int32_t attn_qkv_prepare(const attn_config_t* cfg, int32_t T, const uint16_t* qkv, int64_t qkv_stride,
                          const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* inv_freq,
@@ -142,6 +144,8 @@ int32_t attn_kv_read(const attn_config_t* cfg, int32_t B, int32_t total, const i
  *   out        bf16 [total_q, q_heads, head_dim].
  *   lse        fp32 [total_q, q_heads] or NULL: log of the sum of the
  *              exponentials of the scaled scores.
+ * Probabilities are rounded to bf16 before the second product; scores, maxima,
+ * sums and outputs are fp32, exponentials within 2^-22, outputs rounded once.
  * A non-finite key or value reaches the queries of its own sequence only;
  * within it, it may also reach queries up to 127 positions before it.
  * cfg's page_size and cache_type are checked but not used.
@@ -164,8 +168,11 @@ int32_t attn_prefill(const attn_config_t* cfg, int32_t B, int32_t total_q, int32
  *              as zeros.
  *   q          bf16 rows [B nq, q_heads, head_dim], q_stride apart.
  *   out, lse   as attn_prefill, B nq rows.
- *   ws         scratch of attn_decode_workspace_size bytes; needs no
- *              initialisation and keeps nothing between calls.
+ *   ws         scratch of attn_decode_workspace_size bytes, 256-byte aligned;
+ *              needs no initialisation and keeps nothing between calls.
+ * Probabilities are rounded to bf16 before the second product; with the 8-bit
+ * cache to f16 after they took their value's scale, and queries to f16 after a
+ * power of two brought the row's largest to [1, 2).  The rest as attn_prefill.
  * Rows of a page past the sequence's end may hold anything.  A non-finite
  * key or value in the sequence reaches its own tokens only, of the new ones
  * those before it too.
