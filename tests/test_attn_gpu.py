@@ -355,8 +355,9 @@ def cold_prefills(lens_q, lens_k, hq, hkv, dim, causal, seed, repeats=6, data=No
             first = (out, lse)
             for b in range(len(lens_q)):
                 r, s = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
-                ref = R.attend(q[r], k[s], v[s], scale, prefill_limit(lens_q[b], lens_k[b], causal))
-                R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
+                if lens_q[b]:
+                    ref = R.attend(q[r], k[s], v[s], scale, prefill_limit(lens_q[b], lens_k[b], causal))
+                    R.check_attention(out[r].cpu(), lse[r].cpu(), ref)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
@@ -1056,3 +1057,159 @@ def test_calls_follow_their_stream():
         ref = R.attend(q[b:b + 1], R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n), 0.1, [n])
         for out in outs:
             R.check_attention(out[b:b + 1].cpu(), None, ref)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cache_offsets_past_32_bits(e4m3):
+    """A cache whose last pages lie past 2^32 bytes and elements: written, read
+    back and attended to there as at its beginning."""
+    hq, hkv, dim, page = 8, 2, 256, 128
+    c, pages = m.attn_config(hq, hkv, dim, page, int(e4m3)), (1 << 32) // (hkv * page * dim) + 40
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.empty(pages * hkv * page * dim * (1 if e4m3 else 2), dtype=torch.uint8, device="cuda").view(kind)
+              .view(pages, hkv, page, dim) for _ in "kv")
+    ks, vs = (torch.empty(pages, hkv, page, device="cuda") if e4m3 else None for _ in "kv")
+    g, lens, err = rng(9), [700, 300], err_word()
+    T = sum(lens)
+    qkv = torch.randn(T, (hq + 2 * hkv) * dim, generator=g).bfloat16().cuda()
+    results = []
+    for first in (3, pages - 12):
+        table = (first + torch.randperm(12, generator=rng(4))[:9].int()).cuda()
+        rows = [table[:6], table[6:]]
+        slots = torch.cat([(r.long()[torch.arange(n, device="cuda") // page] * page + torch.arange(n, device="cuda") % page).int()
+                           for r, n in zip(rows, lens)])
+        q = torch.empty(T, hq, dim, dtype=torch.bfloat16, device="cuda")
+        m.attn_qkv_prepare(c, T, qkv, qkv.stride(0), None, None, 0.0, None, 0, 0, 1.0, None, slots, pages, kc, vc, ks, vs, q,
+                           None, err=err)
+        tb = torch.zeros(2, 6, dtype=torch.int32, device="cuda")
+        tb[0], tb[1, :3] = rows[0], rows[1]
+        k, v = (torch.empty(T, hkv, dim, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        m.attn_kv_read(c, 2, T, tb, 6, R.starts(lens).cuda(), pages, kc, vc, ks, vs, k, v, err=err)
+        last = q[torch.tensor([lens[0] - 1, T - 1], device="cuda")]
+        out, ws = torch.empty_like(last), torch.empty(m.attn_decode_workspace_size(c, 2, 1, 700), dtype=torch.uint8, device="cuda")
+        m.attn_decode(c, 2, 1, 700, last, hq * dim, tb, 6, torch.tensor(lens, dtype=torch.int32, device="cuda"), pages, kc, vc,
+                      ks, vs, dim ** -0.5, out, None, ws, err=err)
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        results.append((k, v, out))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    k, v, out = (t.cpu() for t in results[1])
+    x = qkv.cpu().view(T, hq + 2 * hkv, dim).float()
+    for got, ref in ((k, x[:, hq:hq + hkv]), (v, x[:, hq + hkv:])):
+        if e4m3:
+            codes, scale = R.quantised(ref)
+            ref = codes.float() * scale[..., None]
+        assert ((got.double() - ref.double()).abs() <= 2.0 ** -8 * ref.double().abs() * 1.001 + 1e-30).all()
+    for b, s in enumerate((slice(0, 700), slice(700, 1000))):
+        ref = R.attend(x[s][-1:, :hq], k[s], v[s], dim ** -0.5, [lens[b]])
+        # the rows read back were rounded once more to bf16: 2^-8 of scores' and values' sizes
+        assert ((out[b:b + 1].double() - ref[0]).abs() <= (2.0 ** -6 + 2.0 ** -8 * 2 * ref[3][..., None]) * ref[2]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_offsets_past_32_bits(dim):
+    """Packed rows past 2^32 elements of q and out, 2^31 of k and v: the same
+    bits as the same sequence at the beginning."""
+    hq, hkv, n = 4, 2, 300
+    far = (1 << 32) // (hq * dim) + 1000
+    q = torch.empty(far + n, hq, dim, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.empty(far + n, hkv, dim, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    g = rng(dim)
+    for t in (q, k, v):
+        t[:n] = torch.randn(n, *t.shape[1:], generator=g).bfloat16()
+        t[far:] = t[:n]
+    out = torch.empty(far + n, hq, dim, dtype=torch.bfloat16, device="cuda")
+    lse, c, err = torch.empty(far + n, hq, device="cuda"), m.attn_config(hq, hkv, dim), err_word()
+    for first in (0, far):
+        cu = torch.tensor([first, first + n], dtype=torch.int32, device="cuda")
+        m.attn_prefill(c, 1, far + n, far + n, cu, cu, q, hq * dim, k, hkv * dim, v, hkv * dim, dim ** -0.5, True, out, lse,
+                       err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.equal(out[:n], out[far:]) and torch.equal(lse[:n], lse[far:])
+    R.check_attention(out[far:].cpu(), lse[far:].cpu(),
+                      R.attend(q[:n].cpu(), k[:n].cpu(), v[:n].cpu(), dim ** -0.5, prefill_limit(n, n, True)))
+
+
+def test_all_calls_at_once():
+    """Prompts of every head size, decode over both caches, writes and
+    read-backs on streams of their own at the same time: what each gives alone."""
+    def prompt(dim, hq, hkv, lens):
+        g = rng(dim + hq)
+        q, k, v = (torch.randn(sum(lens), h, dim, generator=g).bfloat16().cuda() for h in (hq, hkv, hkv))
+        cu, c = R.starts(lens).cuda(), m.attn_config(hq, hkv, dim)
+
+        def call(out):
+            m.attn_prefill(c, len(lens), q.shape[0], q.shape[0], cu, cu, q, hq * dim, k, hkv * dim, v, hkv * dim, dim ** -0.5,
+                           True, out[0], out[1])
+        return call, [(q.shape, torch.bfloat16), (q.shape[:2], torch.float32)]
+
+    def steps(dim, e4m3, lens, nq):
+        g, hkv, page = rng(dim + nq), 2, 32
+        table, pages = R.make_table(g, lens, page)
+        kd, vd, ksd, vsd = R.cuda(*R.make_cache(g, pages, hkv, page, dim, e4m3))
+        q = torch.randn(len(lens) * nq, 16, dim, generator=g).bfloat16().cuda()
+        c, top = m.attn_config(16, hkv, dim, page, int(e4m3)), max(lens)
+        tb, ln = R.cuda(table, torch.tensor(lens, dtype=torch.int32))
+        ws = torch.empty(m.attn_decode_workspace_size(c, len(lens), nq, top), dtype=torch.uint8, device="cuda")
+        total, cu = sum(lens), R.starts(lens).cuda()
+
+        def call(out):
+            m.attn_decode(c, len(lens), nq, top, q, 16 * dim, tb, tb.stride(0), ln, pages, kd, vd, ksd, vsd, dim ** -0.5,
+                          out[0], out[1], ws)
+            m.attn_kv_read(c, len(lens), total, tb, tb.stride(0), cu, pages, kd, vd, ksd, vsd, out[2], out[3])
+        return call, [(q.shape, torch.bfloat16), (q.shape[:2], torch.float32)] + 2 * [((total, hkv, dim), torch.bfloat16)]
+
+    jobs = [prompt(256, 16, 2, [300, 700]), prompt(128, 16, 16, [600, 1, 90]), prompt(64, 12, 4, [513]),
+            prompt(256, 48, 48, [200, 129]), steps(128, True, [3000, 20, 900], 4), steps(256, False, [77, 2000], 1),
+            steps(64, True, [500] * 40, 8)]
+    fresh = lambda kinds: [torch.full(s, math.nan, dtype=t, device="cuda") for s, t in kinds]  # noqa: E731
+    alone, rounds, streams = [], [], [torch.cuda.Stream() for _ in jobs]
+    for call, kinds in jobs:
+        alone.append(fresh(kinds))
+        call(alone[-1])
+        torch.cuda.synchronize()
+    for _ in range(8):
+        rounds.append([fresh(kinds) for _, kinds in jobs])
+    torch.cuda.synchronize()
+    for outs in rounds:
+        for (call, _), out, s in zip(jobs, outs, streams):
+            with torch.cuda.stream(s):
+                call(out)
+    torch.cuda.synchronize()
+    for outs in rounds:
+        for out, want in zip(outs, alone):
+            assert all(torch.equal(a, b) and torch.isfinite(b.float()).all() for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prefill_captured_and_replayed_twice_at_once(dim):
+    """Two graphs that hold the call, replayed on two streams at the same time
+    with lengths that changed since the capture."""
+    hq, hkv, T, g = 16, 4, 700, rng(dim)
+    q, k, v = (torch.randn(T, h, dim, generator=g).bfloat16().cuda() for h in (hq, hkv, hkv))
+    cu, c = R.starts([300, 400]).cuda(), m.attn_config(hq, hkv, dim)
+    outs = [torch.zeros(T, hq, dim, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+
+    def call(out):
+        m.attn_prefill(c, 2, T, T, cu, cu, q, hq * dim, k, hkv * dim, v, hkv * dim, dim ** -0.5, True, out)
+
+    call(outs[2])
+    torch.cuda.synchronize()
+    graphs = []
+    for out in outs[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(out)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for lens in ([300, 400], [1, 699], [700, 0], [555, 145]):
+        cu.copy_(R.starts(lens))
+        call(outs[2])
+        torch.cuda.synchronize()
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(3):
+                    gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+        R.check_attention(outs[2][:lens[0]].cpu(), None, R.attend(q[:lens[0]].cpu(), k[:lens[0]].cpu(), v[:lens[0]].cpu(),
+                                                                  dim ** -0.5, prefill_limit(lens[0], lens[0], True)))
