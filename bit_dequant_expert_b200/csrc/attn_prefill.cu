@@ -34,6 +34,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.h"
 #include "common.cuh"
@@ -341,7 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // threads hand P over in two parts, the first 32 and the last 32 keys of each half.  Of a tile's last block
                 // only the first `keys` rows of V count (in steps of 16; zero_tail has cleared the rest of the last step, in
                 // place of the whole rest: two of 2049 keys, 16 heads of 128, 50.3 us instead of 57.4).
-                auto product_o = [&](int s, int buf, int first, bool add, uint32_t parity, int keys) {
+                // Where whole blocks, nearly all, are told from last ones hangs on what the issuing warp has to do meanwhile.
+                // 8192 tokens, 16 and 2 heads, us, by a branch around the product, a branch within it and a comparison a
+                // step: heads of 64 217.7, 206.9, 216.4; of 128 226.1, 230.1, 228.3; 4096 after 4096, heads of 256 320, 312,
+                // 312.
+                auto product_of = [&](auto whole, int s, int buf, int first, bool add, uint32_t parity, int keys) {
                     constexpr int kKeys = kN / C::kParts;
                     const uint32_t d = tmem + C::kOCol + s * D, pa = tmem + buf * kN;
                     uint32_t vb[C::kParts];
@@ -360,9 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            vb[kk / (kKeys / 16)] + kk % (kKeys / 16) * (2048 / 16), kHi, kIdO,
                                            add || part + i != 0);
                         };
-                        // head size 64 branches, whose products are too short to hide a comparison each (16 and 2 heads, 8192
-                        // tokens: 206.9 us, with the comparisons alone 216; of 128: 230 with the branch, 227.9 without)
-                        if (D == 64 && keys >= kN) {
+                        if (decltype(whole)::value || (D == 64 && keys >= kN)) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) step(true, i);
                         } else {
@@ -371,6 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     tc_commit_warp(issue, &sm.o_done[buf]);
+                };
+                auto product_o = [&](int s, int buf, int first, bool add, uint32_t parity, int keys) {
+                    if (D == 128 && keys >= kN) product_of(std::true_type{}, s, buf, first, add, parity, keys);
+                    else product_of(std::false_type{}, s, buf, first, add, parity, keys);
                 };
                 // values past the last key that the tile sees, from this row of its last block to the end of the step of 16
                 // that holds it, are zeroed: they may hold NaN, and 0 NaN is NaN
