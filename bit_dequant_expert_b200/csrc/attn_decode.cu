@@ -1,5 +1,6 @@
 // Attention of a few new tokens per sequence over the paged cache: bound by
-// the bytes of the cache, each read once.
+// the bytes of the cache, each read once (more than 64 query rows of a
+// key/value head, or 32 of 256 elements, take a pass for each so many).
 //
 // The nq G query rows (nq tokens, G heads) of a key/value head share its keys.
 // The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so that a
@@ -34,7 +35,7 @@
 //
 // One sequence of 131072 rows of 2 heads of 256 in 8 bits: 27.7 us (4.9 TB/s),
 // 33.7 with the join.  64 ragged sequences up to 16384 of 2 heads of 128 in 8
-// bits, 32 query rows a head: 91 us (3.1 TB/s), with the mma pipe, the issue
+// bits, 32 query rows a head: 93 us (3.0 TB/s), with the mma pipe, the issue
 // slots and the shared memory each busy 37 to 43% of the time: a tile's steps
 // wait for one another.  (More groups, or the queries in registers instead of
 // shared memory: 56 us against 51 at half the lengths.)

@@ -28,8 +28,8 @@
 //
 // Bound by the tensor pipe together with the exponentials, one in 8 clocks of a
 // scheduler: one causal prompt of 16384 tokens, 16 and 2 heads of 128, takes 1.02
-// ms under the power cap (1,075 TFLOP/s; the pipe runs 61% of the time), chunks of
-// 2048 and 1000 tokens after 8192 and 3999, heads of 256, 0.349 ms (1,098; 73%).
+// ms under the power cap (1,075 TFLOP/s; the pipe runs 60% of the time), chunks of
+// 2048 and 1000 tokens after 8192 and 3999, heads of 256, 0.347 ms (1,103; 74%).
 #include <cuda.h>
 #include <math_constants.h>
 
@@ -709,7 +709,7 @@ cudaError_t prefill_dim(const AttnPrefillArgs& a, cudaStream_t st) {
         // all keys.  B200, us (halves, pairs), 16 and 2 heads of 128: one prompt of 300 tokens 10, 13; 2048: 34, 73; 3000:
         // 66, 77; 3200: 68, 77; 4096: 90, 83; 8192: 268, 251.  Two of 1000: 26, 30; of 2000, 20 and 5: 40, 73; of 1500, 100,
         // 30 and 700: 37, 49.  Four of 512: 22, 18; three of 600: 22, 19; sixteen of 200: 39, 25.  (Lost by it: three of
-        // 700: 30, 22; two of 1200: 41, 36.)
+        // 700: 30, 22; two of 1200: 41, 36.)  Head size 64 and other counts of heads go by the same numbers, not measured there.
         const int64_t pairs = most_items(a, 2);
         const bool halves = 2 * pairs <= 148 || (pairs < 212 && a.total_k >= (int64_t)1000 * std::min(a.B, 2));
         return halves ? prefill_mode<D, kHalves>(a, st) : prefill_mode<D, kPairs>(a, st);
