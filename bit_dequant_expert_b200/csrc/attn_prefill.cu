@@ -75,7 +75,7 @@ struct Smem {
     uint8_t q[C::kTiles][C::kQBytes];                         // 1024-aligned, as the slots
     uint8_t slot[C::kSlots][C::kSlot];
     float m[2][kM], top[2][kM];                               // a group's maxima, handed on; between a row's threads
-    uint64_t q_full, slot_full[C::kSlots], slot_empty[C::kSlots];
+    uint64_t q_full, slot_full[C::kSlots], slot_empty[C::kSlots], drained;
     // of each score buffer; p_half: the first 32 of each 64 keys; o_done: the product of its probabilities.  A wait tells a
     // phase from the next one only: each wait below is for the phase after one that its thread knows to be complete
     uint64_t s_full[2], p_half[2], p_full[2], o_done[2], m_full[2];
@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
         mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.drained, 1);
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(&sm.slot_full[i], 1);
             mbar_init(&sm.slot_empty[i], 1);
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int n = 0;   // slots issued so far
                 bool ok = true;
                 auto load = [&](const CUtensorMap* map, int row, int block) {
-                    const int i = n % C::kSlots;
+                    const int i = n % C::kSlots;   // this thread waits for each phase of a slot's barrier in turn
                     if (n >= C::kSlots)
                         ok = ok && mbar_wait_live(&sm.slot_empty[i], (n / C::kSlots - 1) & 1, &sm.dead, a.err);
                     if (!ok) return;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t kIdO = idesc_bf16_f32_bmn(kM, D);
                 bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_live(&sm.q_full, 0, &sm.dead, a.err));
                 int n = 0;   // slots taken so far
-                // waits for the slots of the next K or V block; returns the first's index
+                // waits for the slots of the next K or V block, all in turn; returns the first's index
                 auto take = [&]() {
                     const int first = n;
                     for (int p = 0; p < C::kParts; ++p, ++n)
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         vb[p] = slot_lo + (first + p) % C::kSlots * (C::kSlot / 16) + smem_desc_lo(0, kKeys * 128);
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
+                        // (the buffer's blocks in turn, each of whose phases is waited for)
                         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_live(part ? &sm.p_full[buf] : &sm.p_half[buf], parity,
                                                                           &sm.dead, a.err));
                         tc_fence_after();
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         uint32_t n = 0;                                         // the group's blocks so far
         for (int j = kMode == kPairs ? 0 : grp; j < blocks; j += kStep, ++n) {
-            ok = ok && mbar_wait_live(&sm.s_full[grp], n & 1, &sm.dead, a.err);
+            ok = ok && mbar_wait_live(&sm.s_full[grp], n & 1, &sm.dead, a.err);   // the group's blocks in turn
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc_fence_after();
             uint32_t x[2][32];
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t3 = max3(t3, __uint_as_float(x[1][16 + i]), __uint_as_float(x[1][17 + i]));
             }
             const float top = fmaxf(max3(t0, t1, t2), t3) * sc;
-            if (kMode == kTurns && j > 0) {                     // the maximum as the other group left it
+            if (kMode == kTurns && j > 0) {                     // the maximum as the other group left it, block after block
                 ok = ok && mbar_wait_live(&sm.m_full[grp ^ 1], ((j - 1) >> 1) & 1, &sm.dead, a.err);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 m = sm.m[grp ^ 1][r];
@@ -660,6 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 16) {
         tc_fence_after();
+        if (sm.dead) {   // leave no product in flight behind: nobody has waited for the last ones then
+            tc_commit_warp(elect_lane(), &sm.drained);
+            mbar_wait_bounded(&sm.drained, 0, nullptr);
+        }
         tmem_dealloc(tmem, kTmemCols);
     }
 }
