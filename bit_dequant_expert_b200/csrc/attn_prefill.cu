@@ -28,8 +28,8 @@
 //
 // Bound by the tensor pipe together with the exponentials, one in 8 clocks of a
 // scheduler: one causal prompt of 16384 tokens, 16 and 2 heads of 128, takes 1.02
-// ms under the power cap (1,075 TFLOP/s; the pipe runs 60% of the time), chunks of
-// 2048 and 1000 tokens after 8192 and 3999, heads of 256, 0.347 ms (1,103; 74%).
+// ms under the power cap (1,079 TFLOP/s; the pipe runs 60% of the time), chunks of
+// 2048 and 1000 tokens after 8192 and 3999, heads of 256, 0.344 ms (1,114; 74%).
 #include <cuda.h>
 #include <math_constants.h>
 
