@@ -1213,3 +1213,86 @@ def test_prefill_captured_and_replayed_twice_at_once(dim):
         assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
         R.check_attention(outs[2][:lens[0]].cpu(), None, R.attend(q[:lens[0]].cpu(), k[:lens[0]].cpu(), v[:lens[0]].cpu(),
                                                                   dim ** -0.5, prefill_limit(lens[0], lens[0], True)))
+
+
+@pytest.mark.parametrize("side", ["q", "k"])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_prepare_with_one_side_normalised(side, layout):
+    T, hq, hkv, dim, page = 70, 6, 2, 128, 16
+    c = m.attn_config(hq, hkv, dim, page, m.ATTN_CACHE_E4M3)
+    d = prepare_case(T, hq, hkv, dim, 96, layout, True, page, 5)
+    d["kw" if side == "q" else "qw"] = None
+    check_prepared(c, d, T, 96, layout, run_prepare(c, d, T, 96, layout))
+
+
+def test_prefill_most_sequences():
+    """65535 sequences, most of them empty, some past the 64000th not."""
+    g, B, hq, hkv, dim = rng(3), 65535, 2, 1, 64
+    lens = [0] * B
+    for b in [0, 5, 639, 640, 641, 30000, 64001, 65534] + torch.randint(0, B, (1500,), generator=g).tolist():
+        lens[b] = 1 + b % 3 + (b % 640 == 0) * 150
+    cu = R.starts(lens)
+    T = sum(lens)
+    q, k, v = (torch.randn(T, h, dim, generator=g).bfloat16() for h in (hq, hkv, hkv))
+    qd, kd, vd, cd = R.cuda(q, k, v, cu)
+    out, lse, err = torch.full_like(qd, math.nan), torch.full((T, hq), math.nan, device="cuda"), err_word()
+    m.attn_prefill(m.attn_config(hq, hkv, dim), B, T, T, cd, cd, qd, hq * dim, kd, hkv * dim, vd, hkv * dim, 0.125, True, out,
+                   lse, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    out, lse = out.cpu(), lse.cpu()
+    for b in [i for i, n in enumerate(lens) if n]:
+        r = slice(cu[b], cu[b + 1])
+        R.check_attention(out[r], lse[r], R.attend(q[r], k[r], v[r], 0.125, prefill_limit(lens[b], lens[b], True)))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_most_sequences_with_strided_queries(e4m3):
+    """65535 sequences of up to 40 rows, pages shared, query rows and page
+    tables wider than what the call reads."""
+    g, B, hq, hkv, dim, page, pages = rng(4), 65535, 2, 1, 64, 16, 50
+    kc, vc, ks, vs = R.make_cache(g, pages, hkv, page, dim, e4m3)
+    lens = torch.randint(0, 41, (B,), generator=g).int()
+    table = torch.randint(0, pages, (B, 5), generator=g).int()
+    q = torch.randn(B, hq * dim + 24, generator=g).bfloat16()
+    c = m.attn_config(hq, hkv, dim, page, int(e4m3))
+    qd, tb, ln, kd, vd, ksd, vsd = R.cuda(q, table, lens, kc, vc, ks, vs)
+    ws = torch.empty(m.attn_decode_workspace_size(c, B, 1, 40), dtype=torch.uint8, device="cuda")
+    out, lse, err = torch.full((B, hq, dim), math.nan, dtype=torch.bfloat16, device="cuda"), torch.empty(B, hq, device="cuda"), err_word()
+    m.attn_decode(c, B, 1, 40, qd, q.shape[1], tb, 5, ln, pages, kd, vd, ksd, vsd, 0.125, out, lse, ws, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    out, lse = out.cpu(), lse.cpu()
+    assert torch.isfinite(out.float()).all() and torch.equal(lse.isinf().all(1), lens == 0)
+    for b in [0, 1, 383, 384, 511, 512, B - 1] + torch.randint(0, B, (600,), generator=g).tolist():
+        n = int(lens[b])
+        ref = R.attend(q[b:b + 1, :hq * dim].view(1, hq, dim), R.rows_of(kc, ks, table[b], n), R.rows_of(vc, vs, table[b], n),
+                       0.125, [n])
+        R.check_attention(out[b:b + 1], lse[b:b + 1], ref)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_longest_sequence(e4m3):
+    """2^30 rows, the most that a call takes, beside a short sequence: a page
+    table of 2^23 entries over four pages.  All keys count alike, so the output is
+    the mean of the pages' values, each of which counts equally often."""
+    g, hkv, dim, page = rng(5), 1, 64, 128
+    n = 1 << 30
+    kc, vc, ks, vs = R.make_cache(g, 4, hkv, page, dim, e4m3)
+    c = m.attn_config(2, hkv, dim, page, int(e4m3))
+    table = (torch.arange(2 * (n // page), device="cuda", dtype=torch.int32) % 4).view(2, -1)
+    lens = torch.tensor([n, 512], dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 2, dim, dtype=torch.bfloat16, device="cuda")
+    kd, vd, ksd, vsd = R.cuda(kc, vc, ks, vs)
+    ws = torch.empty(m.attn_decode_workspace_size(c, 2, 1, n), dtype=torch.uint8, device="cuda")
+    out, lse, err = torch.empty_like(q), torch.empty(2, 2, device="cuda"), err_word()
+    m.attn_decode(c, 2, 1, n, q, 2 * dim, table, table.stride(0), lens, 4, kd, vd, ksd, vsd, 0.125, out, lse, ws, err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    values = R.rows_of(vc, vs, torch.arange(4), 512)[:, 0]
+    mean, size = values.mean(0), values.abs().mean(0)
+    # 2^30 terms over 148 blocks, two or three groups and 16 lanes: 2^17 additions a sum of l, 2^17 products of 64 keys a sum
+    # of the output, each off by half a step of what has come together: 2^17 2^-24 = 2^-7 at the worst, all to one side
+    for b, tol in ((0, 2.0 ** -7 + 2.0 ** -8), (1, 2.0 ** -8 + 2.0 ** -12)):
+        assert ((out[b].cpu().double() - mean).abs() <= 2.0 ** -8 * mean.abs() + tol * size).all()
+    assert abs(lse[0, 0].item() - math.log(n)) <= 2.0 ** -7 and abs(lse[1, 0].item() - math.log(512)) <= 2.0 ** -12
